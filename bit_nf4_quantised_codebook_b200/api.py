@@ -17,7 +17,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqlora_nf4.so")
 
 QLORA_OP_QUANTIZE, QLORA_OP_FORWARD, QLORA_OP_BACKWARD, QLORA_OP_MERGE = 0, 1, 2, 3
-QLORA_DEVERR_NONFINITE, QLORA_DEVERR_TIMEOUT = 1, 2
+QLORA_DEVERR_NONFINITE, QLORA_DEVERR_TIMEOUT, QLORA_DEVERR_KV_INDEX = 1, 2, 4
 QLORA_ERR_CUDA = 4
 CODEBOOKS = {"nf4": 0, "int4": 1, "fp4_e2m1": 2, "fp4_e3m0": 3}
 DQ_MODES = {"none": 0, "e4m3": 1, "int8": 2}
@@ -29,6 +29,8 @@ EXPORTED = [
     "qlora_selftest_bounded_wait", "qlora_adamw_step", "qlora_merge_requantize",
     "qlora_format_codebook", "qlora_format_sizes", "qlora_format_workspace_size", "qlora_quantize_format",
     "qlora_dequantize_format", "qlora_quant_error", "qlora_last_cuda_error",
+    "qlora_kv_cache_sizes", "qlora_kv_append", "qlora_kv_read", "qlora_kv_attention_workspace_size",
+    "qlora_kv_attention",
 ]
 
 
@@ -53,6 +55,17 @@ class _Format(ctypes.Structure):
 class _QWeight(ctypes.Structure):
     _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("fmt", _Format), ("codes", ctypes.c_void_p),
                 ("consts", ctypes.c_void_p), ("c1", ctypes.c_void_p), ("mean", ctypes.c_void_p)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int), ("heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("codebook", ctypes.c_int), ("k_codes", ctypes.c_void_p),
+                ("k_absmax", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("v_absmax", ctypes.c_void_p)]
+
+
+class _KVBatch(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("max_pages", ctypes.c_int), ("tokens", ctypes.c_int64),
+                ("token_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p)]
 
 
 _lib = None
@@ -92,6 +105,12 @@ def lib() -> ctypes.CDLL:
         L.qlora_merge_requantize.argtypes = [ctypes.POINTER(_Weight), vp, vp, i32, f32, ctypes.POINTER(_Weight),
                                              vp, vp, sz, vp, vp]
         L.qlora_last_cuda_error.argtypes = [vp]
+        pc, pb = ctypes.POINTER(_KVCache), ctypes.POINTER(_KVBatch)
+        L.qlora_kv_cache_sizes.argtypes = [i64, i32, i32, i32, vp, vp]
+        L.qlora_kv_append.argtypes = [pc, pb, vp, i64, i64, vp, i64, i64, vp, vp]
+        L.qlora_kv_read.argtypes = [pc, pb, vp, vp, vp, vp]
+        L.qlora_kv_attention_workspace_size.argtypes = [pc, i32, i64, i32, vp]
+        L.qlora_kv_attention.argtypes = [pc, pb, vp, i32, i64, i64, f32, i32, i32, vp, vp, sz, vp, vp]
         for name in EXPORTED[1:]:
             if name not in ("qlora_kernel_launch_count", "qlora_last_cuda_error"):
                 getattr(L, name).restype = i32
@@ -415,6 +434,168 @@ def qlora_adamw_step(tensors, lr: float, beta1: float = 0.9, beta2: float = 0.99
     """One AdamW step over up to 16 tensors in one launch (see AdamwGroup for the
     tensor list); for repeated steps on the same tensors, keep an AdamwGroup."""
     AdamwGroup(tensors).step(lr, beta1, beta2, eps, weight_decay, step)
+
+
+# ---------------------------------------------------------------- 4-bit key/value cache
+def _here(t: torch.Tensor, name: str) -> None:
+    """The calls launch on the current device's stream: the tensors must be there."""
+    if t.device.index != torch.cuda.current_device():
+        raise QloraError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+@dataclass
+class KVCache:
+    """A paged cache of keys and values in 4 bits (qlora_kv_cache of the C header).
+    The buffers are kept in place for the cache's lifetime."""
+    num_pages: int
+    page_size: int
+    heads: int                 # key/value heads
+    head_dim: int
+    codebook: str
+    k_codes: torch.Tensor      # uint8 [num_pages, heads, page_size, head_dim / 2]
+    k_absmax: torch.Tensor     # bfloat16 [num_pages, heads, page_size, head_dim / 64]
+    v_codes: torch.Tensor
+    v_absmax: torch.Tensor
+
+    def __post_init__(self):
+        rows = (self.num_pages, self.heads, self.page_size)
+        if self.codebook not in CODEBOOKS:
+            raise QloraError(f"codebook: expected one of {sorted(CODEBOOKS)}, got {self.codebook!r}")
+        _check(lib().qlora_kv_cache_sizes(self.num_pages, self.page_size, self.heads, self.head_dim, None, None),
+               "KVCache")
+        for side in ("k", "v"):
+            codes, absmax = getattr(self, side + "_codes"), getattr(self, side + "_absmax")
+            _need(codes, torch.uint8, rows + (self.head_dim // 2,), side + "_codes")
+            _need(absmax, torch.bfloat16, rows + (self.head_dim // 64,), side + "_absmax")
+            if codes.device != self.k_codes.device or absmax.device != self.k_codes.device:
+                raise QloraError("KVCache: the buffers are on different devices")
+        self._c = _KVCache(self.num_pages, self.page_size, self.heads, self.head_dim, CODEBOOKS[self.codebook],
+                           self.k_codes.data_ptr(), self.k_absmax.data_ptr(), self.v_codes.data_ptr(),
+                           self.v_absmax.data_ptr())
+
+    def nbytes(self) -> int:
+        return 2 * (self.k_codes.numel() + 2 * self.k_absmax.numel())
+
+
+def alloc_kv_cache(num_pages: int, heads: int, head_dim: int, page_size: int = 64, codebook: str = "nf4",
+                   device=None) -> KVCache:
+    """A KVCache with uninitialised pages (slots are read only after they were appended to)."""
+    _check(lib().qlora_kv_cache_sizes(num_pages, page_size, heads, head_dim, None, None), "alloc_kv_cache")
+    dev = device or torch.device("cuda")
+    new = lambda last, dtype: torch.empty(num_pages, heads, page_size, last, dtype=dtype, device=dev)
+    return KVCache(num_pages, page_size, heads, head_dim, codebook, new(head_dim // 2, torch.uint8),
+                   new(head_dim // 64, torch.bfloat16), new(head_dim // 2, torch.uint8),
+                   new(head_dim // 64, torch.bfloat16))
+
+
+@dataclass
+class KVBatch:
+    """The sequences of one call (qlora_kv_batch of the C header), int32 on the device.
+    The arrays may be rewritten in place between calls."""
+    token_start: torch.Tensor  # [batch + 1]: sequence b owns token rows token_start[b] .. token_start[b + 1] - 1
+    kv_len: torch.Tensor       # [batch]: cached tokens, the call's own included
+    page_table: torch.Tensor   # [batch, max_pages]
+
+    def __post_init__(self):
+        if self.page_table.dim() != 2:
+            raise QloraError(f"page_table: expected [batch, max_pages], got {tuple(self.page_table.shape)}")
+        batch, max_pages = self.page_table.shape
+        _need(self.token_start, torch.int32, (batch + 1,), "token_start")
+        _need(self.kv_len, torch.int32, (batch,), "kv_len")
+        _need(self.page_table, torch.int32, (batch, max_pages), "page_table")
+        if len({t.device for t in (self.token_start, self.kv_len, self.page_table)}) != 1:
+            raise QloraError("KVBatch: the arrays are on different devices")
+        self._start, self._len, self._table = (t.data_ptr() for t in (self.token_start, self.kv_len, self.page_table))
+        self.batch, self.max_pages = batch, max_pages
+
+    def c_struct(self, tokens: int) -> _KVBatch:
+        return _KVBatch(self.batch, self.max_pages, tokens, self._start, self._len, self._table)
+
+
+def _kv_devices(cache: KVCache, batch: KVBatch, **tensors) -> None:
+    _here(cache.k_codes, "cache")
+    _here(batch.kv_len, "batch")
+    for name, t in tensors.items():
+        if t is not None and t.device != cache.k_codes.device:
+            raise QloraError(f"{name} is on {t.device}, the cache on {cache.k_codes.device}")
+
+
+def _kv_rows(t: torch.Tensor, heads, head_dim: int, name: str) -> tuple[int, int]:
+    """A bfloat16 [tokens, heads, head_dim] tensor whose channels are contiguous (rows and heads may be
+    strided); returns its row and head strides (0 for an axis of one element)."""
+    if (t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != head_dim or t.stride(2) != 1
+            or (heads is not None and t.shape[1] != heads)):
+        raise QloraError(f"{name}: expected bfloat16 [tokens, {heads if heads is not None else 'heads'}, {head_dim}] "
+                         f"with contiguous channels, got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
+    return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def qlora_kv_append(cache: KVCache, batch: KVBatch, K: torch.Tensor, V: torch.Tensor,
+                    dev_err: torch.Tensor | None = None) -> None:
+    """Quantise K and V (bfloat16 [tokens, heads, head_dim]; rows and heads may be
+    strided) into the last positions of the batch's sequences."""
+    kt, kh = _kv_rows(K, cache.heads, cache.head_dim, "K")
+    vt, vh = _kv_rows(V, cache.heads, cache.head_dim, "V")
+    if K.shape[0] != V.shape[0]:
+        raise QloraError(f"K has {K.shape[0]} token rows, V {V.shape[0]}")
+    _kv_devices(cache, batch, K=K, V=V, dev_err=dev_err)
+    if K.shape[0] == 0:
+        return
+    _check(lib().qlora_kv_append(cache._c, batch.c_struct(K.shape[0]), K.data_ptr(), kt, kh, V.data_ptr(), vt, vh,
+                                 _ptr(dev_err), _stream()), "qlora_kv_append")
+
+
+def qlora_kv_read(cache: KVCache, batch: KVBatch, tokens: int, K_out: torch.Tensor | None = None,
+                  V_out: torch.Tensor | None = None, dev_err: torch.Tensor | None = None):
+    """The stored keys and values of the batch's token rows as bfloat16
+    [tokens, heads, head_dim].  Returns (K_out, V_out), both new unless one is
+    given: then only the given ones are written (the other is None)."""
+    shape = (tokens, cache.heads, cache.head_dim)
+    if K_out is None and V_out is None:
+        K_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
+        V_out = torch.empty_like(K_out)
+    for t, name in ((K_out, "K_out"), (V_out, "V_out")):
+        if t is not None:
+            _need(t, torch.bfloat16, shape, name)
+    _kv_devices(cache, batch, K_out=K_out, V_out=V_out, dev_err=dev_err)
+    if tokens == 0:
+        return K_out, V_out
+    _check(lib().qlora_kv_read(cache._c, batch.c_struct(tokens), _ptr(K_out), _ptr(V_out), _ptr(dev_err),
+                               _stream()), "qlora_kv_read")
+    return K_out, V_out
+
+
+def qlora_kv_attention_workspace_size(cache: KVCache, batch: int, tokens: int, q_heads: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().qlora_kv_attention_workspace_size(cache._c, batch, tokens, q_heads, ctypes.byref(n)),
+           "qlora_kv_attention_workspace_size")
+    return n.value
+
+
+def qlora_kv_attention(cache: KVCache, batch: KVBatch, Q: torch.Tensor, scale: float | None = None,
+                       causal: bool = True, window: int = 0, out: torch.Tensor | None = None,
+                       ws: torch.Tensor | None = None, dev_err: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of Q (bfloat16 [tokens, q_heads, head_dim]; rows and heads may be
+    strided) over the cache; the rows are the last positions of their sequences,
+    already appended.  scale defaults to head_dim ** -0.5; window > 0 limits each
+    row to its last `window` positions.  Returns out, bfloat16
+    [tokens, q_heads, head_dim] (zeros where a row sees nothing)."""
+    qt, qh = _kv_rows(Q, None, cache.head_dim, "Q")
+    tokens, q_heads = Q.shape[0], Q.shape[1]
+    if out is None:
+        out = torch.empty((tokens, q_heads, cache.head_dim), dtype=torch.bfloat16, device=Q.device)
+    _need(out, torch.bfloat16, (tokens, q_heads, cache.head_dim), "out")
+    if ws is None:
+        need = qlora_kv_attention_workspace_size(cache, batch.batch, tokens, q_heads)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=Q.device)
+    _kv_devices(cache, batch, Q=Q, out=out, ws=ws, dev_err=dev_err)
+    if tokens == 0:
+        return out
+    _check(lib().qlora_kv_attention(cache._c, batch.c_struct(tokens), Q.data_ptr(), q_heads, qt, qh,
+                                    cache.head_dim ** -0.5 if scale is None else scale, int(causal),
+                                    window, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                    _ptr(dev_err), _stream()), "qlora_kv_attention")
+    return out
 
 
 def bits_to_tensor(bits, device="cuda") -> torch.Tensor:

@@ -11,6 +11,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include "internal.h"
+#include "kv_common.cuh"
 #include "linear_plan.h"
 #include "nf4_decode.cuh"
 
@@ -151,6 +152,16 @@ qlora_status check_linear(const qlora_nf4_weight *w, int64_t M, int r) {
   if (M < 1 || r < 1) return QLORA_ERR_INVALID_ARG;
   if (r % 8 != 0 || r > 256 || w->N % 8 != 0 || M > (1ll << 30)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   return QLORA_OK;
+}
+
+// Levels of a code book, built once (the NF4 quantiles take tens of microseconds).
+void kv_levels(int codebook, float levels[16]) {
+  static float all[4][16];
+  static std::once_flag once;
+  std::call_once(once, [] {
+    for (int cb = 0; cb < 4; ++cb) build_format_codebook_f32(cb, all[cb], nullptr);
+  });
+  std::memcpy(levels, all[codebook], sizeof(all[codebook]));
 }
 
 std::atomic<uint64_t> g_launches{0};
@@ -517,6 +528,122 @@ qlora_status qlora_linear_backward(const qlora_nf4_weight *w, const uint16_t *X,
   cudaError_t e = run_backward(make_ctx(dev_err, stream), *w, X, dY, M, A, B, r, s, T_saved, dX, dA, dB, pl,
                                static_cast<uint8_t *>(ws));
   return cuda_status(e);
+}
+
+static qlora_status check_kv_shape(int64_t num_pages, int page_size, int heads, int head_dim) {
+  if (num_pages < 1 || page_size < 1 || heads < 1 || head_dim < 1) return QLORA_ERR_INVALID_ARG;
+  if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
+    return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (heads > 512 || num_pages > (1ll << 30)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  return QLORA_OK;
+}
+
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+static qlora_status check_kv(const qlora_kv_cache *c, const qlora_kv_batch *b) {
+  if (!c || !b || !c->k_codes || !c->k_absmax || !c->v_codes || !c->v_absmax) return QLORA_ERR_INVALID_ARG;
+  if (!b->token_start || !b->kv_len || !b->page_table || b->batch < 1 || b->max_pages < 1 || b->tokens < 0)
+    return QLORA_ERR_INVALID_ARG;
+  const qlora_status st = check_kv_shape(c->num_pages, c->page_size, c->heads, c->head_dim);
+  if (st != QLORA_OK) return st;
+  if (c->codebook < QLORA_CB_NF4 || c->codebook > QLORA_CB_FP4_E3M0) return QLORA_ERR_INVALID_ARG;
+  if (b->batch > QLORA_KV_MAX_BATCH || b->tokens > (1ll << 30)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(c->k_codes) || !aligned16(c->k_absmax) || !aligned16(c->v_codes) || !aligned16(c->v_absmax) ||
+      !aligned4(b->token_start) || !aligned4(b->kv_len) || !aligned4(b->page_table))
+    return QLORA_ERR_MISALIGNED;
+  return QLORA_OK;
+}
+
+// A strided [rows][heads][channels] bfloat16 input: 16-byte aligned vectors of 8 channels.
+static qlora_status check_strided(const uint16_t *p, int64_t token_stride, int64_t head_stride) {
+  if (!p || token_stride < 0 || head_stride < 0) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(p) || token_stride % 8 != 0 || head_stride % 8 != 0) return QLORA_ERR_MISALIGNED;
+  return QLORA_OK;
+}
+
+qlora_status qlora_kv_cache_sizes(int64_t num_pages, int page_size, int heads, int head_dim, size_t *codes_bytes,
+                                  size_t *absmax_bytes) {
+  const qlora_status st = check_kv_shape(num_pages, page_size, heads, head_dim);
+  if (st != QLORA_OK) return st;
+  const size_t rows = static_cast<size_t>(num_pages) * page_size * heads;
+  if (codes_bytes) *codes_bytes = rows * (head_dim / 2);
+  if (absmax_bytes) *absmax_bytes = rows * (head_dim / 64) * 2;
+  return QLORA_OK;
+}
+
+qlora_status qlora_kv_append(const qlora_kv_cache *cache, const qlora_kv_batch *batch, const uint16_t *K,
+                             int64_t k_token_stride, int64_t k_head_stride, const uint16_t *V,
+                             int64_t v_token_stride, int64_t v_head_stride, int *dev_err, void *stream) {
+  qlora_status st = check_kv(cache, batch);
+  if (st != QLORA_OK) return st;
+  if ((st = check_strided(K, k_token_stride, k_head_stride)) != QLORA_OK) return st;
+  if ((st = check_strided(V, v_token_stride, v_head_stride)) != QLORA_OK) return st;
+  if (!device_ok()) return QLORA_ERR_NO_DEVICE;
+  if (batch->tokens == 0) return QLORA_OK;
+  static uint32_t tables[4][32];
+  static std::once_flag once;
+  static bool built = true;
+  std::call_once(once, [] {
+    for (int cb = 0; cb < 4; ++cb) built &= build_kv_code_table(cb, tables[cb]);
+  });
+  if (!built) return QLORA_ERR_INVALID_ARG;
+  return cuda_status(launch_kv_append(*cache, kv_device_batch(*cache, *batch, dev_err), K, k_token_stride,
+                                      k_head_stride, V, v_token_stride, v_head_stride, tables[cache->codebook],
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+qlora_status qlora_kv_read(const qlora_kv_cache *cache, const qlora_kv_batch *batch, uint16_t *K_out,
+                           uint16_t *V_out, int *dev_err, void *stream) {
+  const qlora_status st = check_kv(cache, batch);
+  if (st != QLORA_OK) return st;
+  if (!K_out && !V_out) return QLORA_ERR_INVALID_ARG;
+  if ((K_out && !aligned16(K_out)) || (V_out && !aligned16(V_out))) return QLORA_ERR_MISALIGNED;
+  if (!device_ok()) return QLORA_ERR_NO_DEVICE;
+  if (batch->tokens == 0) return QLORA_OK;
+  float levels[16];
+  kv_levels(cache->codebook, levels);
+  return cuda_status(launch_kv_read(*cache, kv_device_batch(*cache, *batch, dev_err), K_out, V_out, levels,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+qlora_status qlora_kv_attention_workspace_size(const qlora_kv_cache *cache, int batch, int64_t tokens, int q_heads,
+                                               size_t *bytes) {
+  if (!cache || !bytes || batch < 1 || tokens < 0 || q_heads < 1) return QLORA_ERR_INVALID_ARG;
+  const qlora_status st = check_kv_shape(cache->num_pages, cache->page_size, cache->heads, cache->head_dim);
+  if (st != QLORA_OK) return st;
+  if (batch > QLORA_KV_MAX_BATCH || q_heads % cache->heads != 0 || q_heads / cache->heads > 128 ||
+      tokens * (q_heads / cache->heads) > (1ll << 30))
+    return QLORA_ERR_UNSUPPORTED_SHAPE;
+  *bytes = kv_attention_workspace(cache->head_dim, device_sms());
+  return QLORA_OK;
+}
+
+qlora_status qlora_kv_attention(const qlora_kv_cache *cache, const qlora_kv_batch *batch, const uint16_t *Q,
+                                int q_heads, int64_t q_token_stride, int64_t q_head_stride, float scale, int causal,
+                                int window, uint16_t *out, void *ws, size_t ws_bytes, int *dev_err, void *stream) {
+  qlora_status st = check_kv(cache, batch);
+  if (st != QLORA_OK) return st;
+  if (!out || q_heads < 1 || window < 0 || !(scale > 0.0f) || std::isinf(scale)) return QLORA_ERR_INVALID_ARG;
+  if ((st = check_strided(Q, q_token_stride, q_head_stride)) != QLORA_OK) return st;
+  size_t need = 0;
+  if ((st = qlora_kv_attention_workspace_size(cache, batch->batch, batch->tokens, q_heads, &need)) != QLORA_OK)
+    return st;
+  if (!aligned16(out)) return QLORA_ERR_MISALIGNED;
+  if (batch->tokens > 0) {
+    const int64_t last = (batch->tokens - 1) * q_token_stride + (q_heads - 1) * q_head_stride + cache->head_dim;
+    const int64_t out_elems = batch->tokens * q_heads * cache->head_dim;
+    if (overlap(Q, static_cast<size_t>(last) * 2, out, static_cast<size_t>(out_elems) * 2)) return QLORA_ERR_INVALID_ARG;
+  }
+  if (!device_ok()) return QLORA_ERR_NO_DEVICE;
+  if (!ws || ws_bytes < need) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(ws)) return QLORA_ERR_MISALIGNED;
+  if (batch->tokens == 0) return QLORA_OK;
+  float levels[16];
+  kv_levels(cache->codebook, levels);
+  return cuda_status(launch_kv_attention(*cache, kv_device_batch(*cache, *batch, dev_err), Q, q_heads,
+                                         q_token_stride, q_head_stride, scale, causal, std::min(window, 1 << 30), out,
+                                         ws, levels, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 uint64_t qlora_kernel_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

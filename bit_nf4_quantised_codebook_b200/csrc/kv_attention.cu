@@ -1,0 +1,833 @@
+// kv_attention.cu — softmax attention of a call's token rows over the 4-bit paged
+// cache, without writing a dequantised key or value anywhere.
+//
+//   s_ij = scale * sum_b cK[j,b] * (sum_{d in b} q_id * levelK_jd)     b: blocks of 64 channels
+//   o_id = sum_j softmax(s_i)_j * cV[j,b] * levelV_jd
+//
+// The constants c multiply sums and weights, never single elements: an element costs
+// one byte-permute and one shared-memory lookup per pair of codes.  A table of 256
+// half2 entries (both levels of a byte), one copy per lane, is laid out so that the
+// permute that picks the byte out of a code word builds the lookup's address in the
+// same instruction (entry stride 256 bytes, table at a multiple of 64 KiB) and 32 lanes
+// never share a bank.  The products run on mma.sync m16n8k16: with a handful of query
+// rows per key/value head the tensor pipe is not what bounds this kernel, and the
+// register layouts of its operands let the codes go from global memory to registers
+// with no staging:
+//   S^T (16 tokens x 8 rows) = K (A operand: token rows, codes decoded in place) * Q^T
+//   O^T (16 channels x 8 rows) += V^T (A operand: pairs of tokens of one channel per
+//        register, formed by merging the nibbles of two tokens' words) * P^T
+// P^T is S^T's accumulator transposed with movmatrix.
+//
+// Numbers.  Levels are held in fp16: exactly for the integer and float grids (stored as
+// the small integers they are multiples of), within 2^-12 for NF4.  Each query row is
+// scaled by a power of two to a largest magnitude in [2^13, 2^14) and is then exact in
+// fp16 down to 2^-38 of it.  Softmax weights enter the second product as
+// w = 2^(s + log2 cV - M_b + 6) in fp16 (within 2^-12), M_b being a running maximum of
+// s + log2 cV per row and block that lags by at most 8: what is below 2^-31 of the
+// largest contribution to a channel block is lost, whatever the constants' range.  The
+// running maximum and sum of the softmax itself and all accumulators are float32.
+//
+// Work.  An item is one sequence x row tile (8 * NT rows: tokens x the query heads of one
+// key/value head) x key/value head, cut into steps of 128 tokens.  The steps of all items
+// form one line that is cut evenly among all warp groups (4 warps; one CTA per SM), so
+// sequences of any mix of lengths finish together.  Inside a step every warp takes 32
+// tokens with its own running statistics; a group joins its four warps through shared
+// memory at the end of its part of an item.  An item that several groups shared is joined
+// from their normalised parts, in order, by a second small kernel.
+#include <atomic>
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include "internal.h"
+#include "kv_common.cuh"
+#include "launch.cuh"
+
+namespace qlora {
+namespace {
+
+constexpr int kStepTokens = 128;     // tokens of one step of a group (4 warps x 32)
+constexpr float kLag = 8.0f;         // a running maximum is renewed when passed by this much (log2)
+constexpr float kLift = 6.0f;        // weights are stored times 2^kLift
+constexpr float kFloor = -3.0e38f;   // "no maximum yet": finite, so that differences stay defined
+
+struct KvAttnArgs {
+  KvBatch kb;
+  const uint16_t *Q;
+  int64_t q_token_stride, q_head_stride;
+  uint16_t *out;
+  const uint8_t *k_codes, *v_codes;
+  const uint16_t *k_absmax, *v_absmax;
+  int heads, group;   // key/value heads; query heads of each
+  float scale_log2;   // scale * log2(e) / unit
+  float v_unit;       // 1 / unit: levels are stored times `unit`
+  int causal, window;
+  __half levels[16];
+  // workspace
+  float *part_o;      // [groups][2][8 * NT][D] normalised partial outputs
+  float *part_lse;    // [groups][2][8 * NT] log2 of their weights' sum
+  struct KvPart *parts;  // [groups][2]
+};
+
+// A group's part of an item that it shares with others (slot 0: the item its range
+// starts in; slot 1: the one it ends in).
+struct KvPart {
+  int64_t first, end;  // the item's steps on the line; end = 0: nothing here
+  int64_t begin;       // the group's first step of it
+  int64_t total;       // steps of the whole line
+  int b, head, tile, pad;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+// Table entry of byte I of w (lane address `tab`: table base | lane * 4).
+template <int I>
+__device__ __forceinline__ uint32_t lookup(uint32_t w, uint32_t tab) {
+  return lds32(prmt(w, tab, 0x7604u | (I << 4)));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Loads of the cache: read once by this SM, so not kept in L1.
+__device__ __forceinline__ uint2 ld_codes2(const uint8_t *p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_codes1(const uint8_t *p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+template <int NB>
+__device__ __forceinline__ void ld_consts(const uint16_t *p, uint32_t (&c)[(NB + 1) / 2]) {
+  if (NB == 1) c[0] = __ldg(p);
+  if (NB == 2) c[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+  if (NB == 4) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+    c[0] = v.x;
+    c[(NB + 1) / 2 - 1] = v.y;
+  }
+}
+template <int NB>
+__device__ __forceinline__ float const_of(const uint32_t (&c)[(NB + 1) / 2], int b) {
+  return __uint_as_float(b & 1 ? c[b / 2] & 0xFFFF0000u : c[b / 2] << 16);
+}
+
+// Steps, row tiles and first token of a sequence's items.
+struct KvSpan {
+  KvSeq q;
+  int tiles;   // row tiles per key/value head (0: no rows)
+  int steps;   // steps of each item (at least 1 where there are rows)
+  int lo;      // first cached token that a row may see, rounded down to 32
+};
+__device__ __forceinline__ KvSpan kv_span(const KvAttnArgs &a, int b, int tile_rows) {
+  KvSpan s;
+  s.q = kv_seq(a.kb, b);
+  s.tiles = static_cast<int>((static_cast<int64_t>(s.q.n) * a.group + tile_rows - 1) / tile_rows);
+  int lo = 0;
+  if (a.window > 0) lo = max(0, min(s.q.len, s.q.pos0() - a.window + 1)) & ~31;
+  s.lo = lo;
+  s.steps = max(1, (s.q.len - lo + kStepTokens - 1) / kStepTokens);
+  return s;
+}
+
+template <int D_, int NT_, int GROUPS_>
+struct AttnCfg {
+  static constexpr int D = D_;
+  static constexpr int NT = NT_;          // tiles of 8 query rows
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int NB = D / 64;       // blocks of 64 channels
+  static constexpr int GROUPS = GROUPS_;  // warp groups per CTA
+  static constexpr int THREADS = GROUPS * 128;
+  static constexpr int T = D == 256 ? 1 : 2;  // tiles of 16 tokens loaded together
+  static constexpr int CW = (NB + 1) / 2;     // words of a token's constants
+  static constexpr int JOIN_FLOATS = 4 * ROWS * D;  // one group's four warps
+  static constexpr int LSE_FLOATS = 4 * ROWS;
+  static constexpr int SMEM_BYTES = 0x20000 + GROUPS * (JOIN_FLOATS + LSE_FLOATS) * 4;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_constant__ KvAttnArgs a) {
+  constexpr int D = C::D, NT = C::NT, NB = C::NB, T = C::T, CW = C::CW, ROWS = C::ROWS;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t smem_base = smem_u32(smem);
+  const uint32_t table = (smem_base + 0xFFFFu) & ~0xFFFFu;  // 64 KiB at a multiple of 64 KiB
+  // before the table: the line's prefix sums; after it: the groups' joins
+  int64_t *prefix = reinterpret_cast<int64_t *>(smem);
+  float *join = reinterpret_cast<float *>(smem + (table - smem_base) + 0x10000u);
+  __shared__ int64_t s_warp_sum[C::THREADS / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gq = warp >> 2, gw = warp & 3;  // group in the CTA, warp in the group
+  const int g = lane >> 2, t = lane & 3;
+  for (int i = tid; i < 256 * 32; i += C::THREADS) {
+    const int byte = i >> 5;
+    const __half2 h = __halves2half2(a.levels[byte >> 4], a.levels[byte & 15]);
+    *reinterpret_cast<__half2 *>(smem + (table - smem_base) + byte * 256 + (i & 31) * 4) = h;
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (table - smem_base < (a.kb.batch + 1) * sizeof(int64_t)) {  // cannot happen while shared memory starts low
+    if (tid < C::GROUPS * 2) a.parts[blockIdx.x * C::GROUPS * 2 + tid].end = 0;
+    kv_error(a.kb);
+    return;
+  }
+
+  // ---------------------------------------------------------------- the line of steps
+  {
+    const int per = (a.kb.batch + C::THREADS - 1) / C::THREADS;
+    const int b0 = min(a.kb.batch, tid * per), b1 = min(a.kb.batch, b0 + per);
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      const KvSpan s = kv_span(a, b, ROWS);
+      sum += static_cast<int64_t>(s.tiles) * a.heads * s.steps;
+    }
+    int64_t x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp_sum[warp] = x;
+    __syncthreads();
+    int64_t at = x - sum;
+    for (int w = 0; w < warp; ++w) at += s_warp_sum[w];
+    for (int b = b0; b < b1; ++b) {
+      prefix[b] = at;
+      const KvSpan s = kv_span(a, b, ROWS);
+      at += static_cast<int64_t>(s.tiles) * a.heads * s.steps;
+    }
+    if (tid == C::THREADS - 1) prefix[a.kb.batch] = at;
+    __syncthreads();
+  }
+  const int64_t total = prefix[a.kb.batch];
+  const int64_t workers = static_cast<int64_t>(gridDim.x) * C::GROUPS;
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * C::GROUPS + gq;
+  int64_t at = me * total / workers;
+  const int64_t stop = (me + 1) * total / workers;
+  const int64_t begin = at;
+  float *my_join = join + gq * (C::JOIN_FLOATS + C::LSE_FLOATS);
+  float *my_lse = my_join + C::JOIN_FLOATS;
+  const uint32_t tab = table | (lane * 4);
+  if (gw == 0 && lane < 2) {  // no part yet
+    a.parts[me * 2 + lane].end = 0;
+    a.parts[me * 2 + lane].total = total;
+  }
+
+  int b = 0;
+  if (at < stop) {  // last b with prefix[b] <= at (sequences without rows take no steps)
+    int lo = 0, hi = a.kb.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= at) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+  }
+  while (at < stop) {
+    while (prefix[b + 1] <= at) ++b;
+    const KvSpan sp = kv_span(a, b, ROWS);
+    const int64_t rel = at - prefix[b];
+    const int item = static_cast<int>(rel / sp.steps);
+    const int step0 = static_cast<int>(rel - static_cast<int64_t>(item) * sp.steps);
+    const int head = item % a.heads, tile = item / a.heads;
+    const int64_t first = prefix[b] + static_cast<int64_t>(item) * sp.steps, end = first + sp.steps;
+    const int step1 = stop < end ? static_cast<int>(stop - first) : sp.steps;
+    const int row_limit = sp.q.n * a.group - tile * ROWS;  // rows of the tile that exist
+
+    // ------------------------------------------------------------ query rows -> B operand
+    uint32_t q[NT][NB][4][2];
+    float qs[NT][2];       // factor of the scores of rows 2t, 2t + 1
+    int see_lo[NT][2], see_hi[NT][2];
+    int all_lo = 0, all_hi = 0x7FFFFFFF;  // tokens that every row sees
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = n * 8 + g;
+      const bool live = r < row_limit;
+      const int rr = tile * ROWS + r;
+      const int i = live ? rr / a.group : 0;
+      const int h = live ? rr - i * a.group : 0;
+      const uint16_t *src = a.Q + static_cast<int64_t>(sp.q.row0 + i) * a.q_token_stride +
+                            static_cast<int64_t>(head * a.group + h) * a.q_head_stride + 16 * t;
+      uint32_t raw[NB][8];
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        uint4 u = make_uint4(0, 0, 0, 0), v = u;
+        if (live) {
+          u = __ldg(reinterpret_cast<const uint4 *>(src + 64 * k));
+          v = __ldg(reinterpret_cast<const uint4 *>(src + 64 * k + 8));
+        }
+        raw[k][0] = u.x, raw[k][1] = u.y, raw[k][2] = u.z, raw[k][3] = u.w;
+        raw[k][4] = v.x, raw[k][5] = v.y, raw[k][6] = v.z, raw[k][7] = v.w;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) m = __vmaxu2(m, raw[k][x] & 0x7FFF7FFFu);
+      }
+      m = max(m >> 16, m & 0xFFFFu);
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      // q * 2^-e has its largest magnitude in [2^13, 2^14); e within what float32 powers hold
+      int e = static_cast<int>(m >> 7) - 127 - 13;
+      if (m == 0 || m >= 0x7F80u) e = 0;
+      e = max(e, -120);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+          q[n][k][x >> 1][x & 1] = pack_half2(__uint_as_float(raw[k][x] << 16) * down,
+                                              __uint_as_float(raw[k][x] & 0xFFFF0000u) * down);
+      float up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * a.scale_log2;
+      if (m >= 0x7F80u) up = __uint_as_float(0x7FC00000u);  // a non-finite query: its row is NaN throughout
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        qs[n][c] = __shfl_sync(0xFFFFFFFFu, up, (2 * t + c) * 4);
+        const int ic = __shfl_sync(0xFFFFFFFFu, i, (2 * t + c) * 4);
+        const int lc = __shfl_sync(0xFFFFFFFFu, live ? 1 : 0, (2 * t + c) * 4);
+        const int pos = sp.q.pos0() + ic;
+        see_hi[n][c] = a.causal ? min(sp.q.len, pos + 1) : sp.q.len;
+        see_lo[n][c] = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+        if (lc) {
+          all_lo = max(all_lo, see_lo[n][c]);
+          all_hi = min(all_hi, see_hi[n][c]);
+        }
+      }
+    }
+    all_lo = __reduce_max_sync(0xFFFFFFFFu, all_lo);
+    all_hi = __reduce_min_sync(0xFFFFFFFFu, all_hi);
+
+    float o[NT][NB][4][4];
+    float l[NT][2], mx[NT][2], mv[NT][NB][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[n][c] = 0.0f;
+        mx[n][c] = kFloor;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) mv[n][k][c] = kFloor;
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[n][k][i][c] = 0.0f;
+    }
+
+    // ------------------------------------------------------------ the steps
+    // This warp's 32-token chunks lie 128 apart; a chunk is worked off in 2 / T parts of T
+    // tiles of 16 tokens.  The codes of the next part are loaded as soon as the registers of
+    // this one are free: keys after the first product, values after the second.
+    constexpr int PARTS = 2 / T;
+    const int units = (step1 - step0) * PARTS;
+    const int64_t page_rows_shift = a.kb.page_shift;
+    uint2 kc[T][2][NB];
+    uint32_t kcon[T][2][CW];
+    uint32_t vc[T][4][NB];
+    uint32_t vcon[T][2][CW];
+    auto base_of = [&](int u) {
+      return sp.lo + (step0 + u / PARTS) * kStepTokens + gw * 32 + (u % PARTS) * (T * 16);
+    };
+    // flat cache row of token 0 of tile i, or -1 (a tile never crosses a page)
+    auto tile_row = [&](int tok) -> int64_t {
+      if (tok >= sp.q.len) return -1;
+      const int page = kv_page(a.kb, b, tok);
+      if (page < 0) {
+        kv_error(a.kb);
+        return -1;
+      }
+      return ((static_cast<int64_t>(page) * a.heads + head) << page_rows_shift) +
+             (tok & ((1 << a.kb.page_shift) - 1));
+    };
+    auto load_k = [&](int i, int tok, int64_t row) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const bool in = row >= 0 && tok + g + 8 * x < sp.q.len;
+        const int64_t rr = row + g + 8 * x;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          kc[i][x][k] = make_uint2(0, 0);
+          if (in) kc[i][x][k] = ld_codes2(a.k_codes + rr * (D / 2) + 32 * k + 8 * t);
+        }
+#pragma unroll
+        for (int k = 0; k < CW; ++k) kcon[i][x][k] = 0;
+        if (in) ld_consts<NB>(a.k_absmax + rr * NB, kcon[i][x]);
+      }
+    };
+    auto load_v = [&](int i, int tok, int64_t row) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int tt = 2 * t + (x & 1) + 8 * (x >> 1);
+        const bool in = row >= 0 && tok + tt < sp.q.len;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          vc[i][x][k] = 0;
+          if (in) vc[i][x][k] = ld_codes1(a.v_codes + (row + tt) * (D / 2) + 32 * k + 4 * g);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const bool in = row >= 0 && tok + g + 8 * x < sp.q.len;
+#pragma unroll
+        for (int k = 0; k < CW; ++k) vcon[i][x][k] = 0;
+        if (in) ld_consts<NB>(a.v_absmax + (row + g + 8 * x) * NB, vcon[i][x]);
+      }
+    };
+    int64_t row[T];
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      const int tok = base_of(0) + 16 * i;
+      row[i] = tile_row(tok);
+      load_k(i, tok, row[i]);
+      load_v(i, tok, row[i]);
+    }
+    for (int u = 0; u < units; ++u) {
+      const int tok0 = base_of(u);
+      const int tok1 = base_of(u + 1);
+      const bool more = u + 1 < units;
+      int64_t next[T];
+#pragma unroll
+      for (int i = 0; i < T; ++i) next[i] = more ? tile_row(tok1 + 16 * i) : -1;
+      // scores: s[i][n][0..3] = (token g, row 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1)
+      float s[T][NT][4];
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[i][n][c] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          float acc[NT][4];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[n][c] = 0.0f;
+          const uint2 w0 = kc[i][0][k], w1 = kc[i][1][k];
+          {
+            const uint32_t a0 = lookup<0>(w0.x, tab), a1 = lookup<0>(w1.x, tab), a2 = lookup<1>(w0.x, tab),
+                           a3 = lookup<1>(w1.x, tab);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(acc[n], a0, a1, a2, a3, q[n][k][0][0], q[n][k][0][1]);
+          }
+          {
+            const uint32_t a0 = lookup<2>(w0.x, tab), a1 = lookup<2>(w1.x, tab), a2 = lookup<3>(w0.x, tab),
+                           a3 = lookup<3>(w1.x, tab);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(acc[n], a0, a1, a2, a3, q[n][k][1][0], q[n][k][1][1]);
+          }
+          {
+            const uint32_t a0 = lookup<0>(w0.y, tab), a1 = lookup<0>(w1.y, tab), a2 = lookup<1>(w0.y, tab),
+                           a3 = lookup<1>(w1.y, tab);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(acc[n], a0, a1, a2, a3, q[n][k][2][0], q[n][k][2][1]);
+          }
+          {
+            const uint32_t a0 = lookup<2>(w0.y, tab), a1 = lookup<2>(w1.y, tab), a2 = lookup<3>(w0.y, tab),
+                           a3 = lookup<3>(w1.y, tab);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(acc[n], a0, a1, a2, a3, q[n][k][3][0], q[n][k][3][1]);
+          }
+          const float c0 = const_of<NB>(kcon[i][0], k), c1 = const_of<NB>(kcon[i][1], k);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            s[i][n][0] = fmaf(c0, acc[n][0], s[i][n][0]);
+            s[i][n][1] = fmaf(c0, acc[n][1], s[i][n][1]);
+            s[i][n][2] = fmaf(c1, acc[n][2], s[i][n][2]);
+            s[i][n][3] = fmaf(c1, acc[n][3], s[i][n][3]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          s[i][n][0] *= qs[n][0];
+          s[i][n][1] *= qs[n][1];
+          s[i][n][2] *= qs[n][0];
+          s[i][n][3] *= qs[n][1];
+        }
+      }
+      if (more) {
+#pragma unroll
+        for (int i = 0; i < T; ++i) load_k(i, tok1 + 16 * i, next[i]);
+      }
+      // masks: only where some row does not see the whole part
+      if (tok0 < all_lo || tok0 + T * 16 > all_hi) {
+#pragma unroll
+        for (int i = 0; i < T; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int j = tok0 + 16 * i + g + 8 * (c >> 1);
+              if (j >= see_hi[n][c & 1] || j < see_lo[n][c & 1]) s[i][n][c] = -INFINITY;
+            }
+      }
+      // running maxima: of s, and of s + log2 cV for each block
+      float lv[T][2][NB];
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int k = 0; k < NB; ++k) lv[i][x][k] = lg2(const_of<NB>(vcon[i][x], k));
+      bool renew = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = s[0][n][c];
+#pragma unroll
+          for (int i = 0; i < T; ++i) top = fmaxf(top, fmaxf(s[i][n][c], s[i][n][c + 2]));
+          renew |= top > mx[n][c] + kLag;
+#pragma unroll
+          for (int k = 0; k < NB; ++k) {
+            float tv = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < T; ++i) tv = fmaxf(tv, fmaxf(s[i][n][c] + lv[i][0][k], s[i][n][c + 2] + lv[i][1][k]));
+            renew |= tv > mv[n][k][c] + kLag;
+          }
+        }
+      if (__any_sync(0xFFFFFFFFu, renew)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float top = mx[n][c];
+#pragma unroll
+            for (int i = 0; i < T; ++i) top = fmaxf(top, fmaxf(s[i][n][c], s[i][n][c + 2]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            l[n][c] *= ex2(mx[n][c] - top);
+            mx[n][c] = top;
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+              float tv = mv[n][k][c];
+#pragma unroll
+              for (int i = 0; i < T; ++i) tv = fmaxf(tv, fmaxf(s[i][n][c] + lv[i][0][k], s[i][n][c + 2] + lv[i][1][k]));
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) tv = fmaxf(tv, __shfl_xor_sync(0xFFFFFFFFu, tv, d));
+              const float f = ex2(mv[n][k][c] - tv);
+              mv[n][k][c] = tv;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                o[n][k][i][c] *= f;
+                o[n][k][i][c + 2] *= f;
+              }
+            }
+          }
+      }
+      // weights and the second product
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          l[n][0] += ex2(s[i][n][0] - mx[n][0]) + ex2(s[i][n][2] - mx[n][0]);
+          l[n][1] += ex2(s[i][n][1] - mx[n][1]) + ex2(s[i][n][3] - mx[n][1]);
+        }
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          uint32_t p[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              // a token that a row does not see adds nothing, whatever its value's constant
+              const float s0 = s[i][n][2 * x], s1 = s[i][n][2 * x + 1], add = lv[i][x][k] + kLift;
+              const float w0 = s0 == -INFINITY ? 0.0f : ex2(s0 + add - mv[n][k][0]);
+              const float w1 = s1 == -INFINITY ? 0.0f : ex2(s1 + add - mv[n][k][1]);
+              p[n][x] = movmatrix(pack_half2(w0, w1));
+            }
+          }
+          // even channels of tokens 2t, 2t + 1 in one byte (x), odd ones in another (y)
+          const uint32_t v0 = vc[i][0][k], v1 = vc[i][1][k], v2 = vc[i][2][k], v3 = vc[i][3][k];
+          const uint32_t x0 = (v0 & 0xF0F0F0F0u) | ((v1 >> 4) & 0x0F0F0F0Fu);
+          const uint32_t y0 = ((v0 << 4) & 0xF0F0F0F0u) | (v1 & 0x0F0F0F0Fu);
+          const uint32_t x1 = (v2 & 0xF0F0F0F0u) | ((v3 >> 4) & 0x0F0F0F0Fu);
+          const uint32_t y1 = ((v2 << 4) & 0xF0F0F0F0u) | (v3 & 0x0F0F0F0Fu);
+          {
+            const uint32_t a0 = lookup<0>(x0, tab), a1 = lookup<0>(y0, tab), a2 = lookup<0>(x1, tab),
+                           a3 = lookup<0>(y1, tab);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(o[n][k][0], a0, a1, a2, a3, p[n][0], p[n][1]);
+          }
+          {
+            const uint32_t a0 = lookup<1>(x0, tab), a1 = lookup<1>(y0, tab), a2 = lookup<1>(x1, tab),
+                           a3 = lookup<1>(y1, tab);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(o[n][k][1], a0, a1, a2, a3, p[n][0], p[n][1]);
+          }
+          {
+            const uint32_t a0 = lookup<2>(x0, tab), a1 = lookup<2>(y0, tab), a2 = lookup<2>(x1, tab),
+                           a3 = lookup<2>(y1, tab);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(o[n][k][2], a0, a1, a2, a3, p[n][0], p[n][1]);
+          }
+          {
+            const uint32_t a0 = lookup<3>(x0, tab), a1 = lookup<3>(y0, tab), a2 = lookup<3>(x1, tab),
+                           a3 = lookup<3>(y1, tab);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(o[n][k][3], a0, a1, a2, a3, p[n][0], p[n][1]);
+          }
+        }
+      }
+      if (more) {
+#pragma unroll
+        for (int i = 0; i < T; ++i) load_v(i, tok1 + 16 * i, next[i]);
+      }
+    }
+
+    // ------------------------------------------------------------ join the group's warps
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float sum = l[n][c];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        const int r = n * 8 + 2 * t + c;
+        const float inv = sum > 0.0f || sum != sum ? a.v_unit / sum : 0.0f;
+        if (g == 0) my_lse[gw * ROWS + r] = sum > 0.0f || sum != sum ? mx[n][c] + lg2(sum) : -INFINITY;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          // channels 8g .. 8g + 7 of block k; M_b - m is at most log2 of the largest constant plus the lag
+          // (past float32's exponents when the constant is near its largest: applied as two halves)
+          const float f = mv[n][k][c] > kFloor ? ex2(0.5f * (mv[n][k][c] - mx[n][c] - kLift)) : 0.0f;
+          const float fi = f * inv;
+          float *dst = my_join + (gw * ROWS + r) * D + 64 * k + 8 * g;
+          *reinterpret_cast<float4 *>(dst) = make_float4(o[n][k][0][c] * fi * f, o[n][k][0][c + 2] * fi * f,
+                                                         o[n][k][1][c] * fi * f, o[n][k][1][c + 2] * fi * f);
+          *reinterpret_cast<float4 *>(dst + 4) = make_float4(o[n][k][2][c] * fi * f, o[n][k][2][c + 2] * fi * f,
+                                                             o[n][k][3][c] * fi * f, o[n][k][3][c + 2] * fi * f);
+        }
+      }
+    named_barrier(1 + gq, 128);
+    const bool whole = step0 == 0 && step1 == sp.steps;
+    const int slot = at == begin ? 0 : 1;
+    const int64_t part = me * 2 + slot;
+    const int tl = tid & 127;
+    for (int x = tl; x < ROWS * (D / 8); x += 128) {
+      const int r = x / (D / 8), ch = (x % (D / 8)) * 8;
+      float top = my_lse[r], wsum = 0.0f;
+#pragma unroll
+      for (int w = 1; w < 4; ++w) top = fmaxf(top, my_lse[w * ROWS + r]);
+      float acc[8] = {};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float lse = my_lse[w * ROWS + r];
+        const float f = lse == -INFINITY ? 0.0f : ex2(lse - top);
+        wsum += f;
+        const float4 u = *reinterpret_cast<const float4 *>(my_join + (w * ROWS + r) * D + ch);
+        const float4 v = *reinterpret_cast<const float4 *>(my_join + (w * ROWS + r) * D + ch + 4);
+        acc[0] = fmaf(f, u.x, acc[0]);
+        acc[1] = fmaf(f, u.y, acc[1]);
+        acc[2] = fmaf(f, u.z, acc[2]);
+        acc[3] = fmaf(f, u.w, acc[3]);
+        acc[4] = fmaf(f, v.x, acc[4]);
+        acc[5] = fmaf(f, v.y, acc[5]);
+        acc[6] = fmaf(f, v.z, acc[6]);
+        acc[7] = fmaf(f, v.w, acc[7]);
+      }
+      const float inv = wsum == 0.0f ? 0.0f : 1.0f / wsum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] *= inv;
+      if (!whole) {
+        float *dst = a.part_o + (part * ROWS + r) * D + ch;
+        *reinterpret_cast<float4 *>(dst) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        *reinterpret_cast<float4 *>(dst + 4) = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (ch == 0) a.part_lse[part * ROWS + r] = wsum == 0.0f ? -INFINITY : top + lg2(wsum);
+      } else if (r < row_limit) {
+        const int rr = tile * ROWS + r, i = rr / a.group, h = rr - i * a.group;
+        uint16_t *dst = a.out +
+                        (static_cast<int64_t>(sp.q.row0 + i) * a.heads * a.group + head * a.group + h) * D + ch;
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]),
+                                                     pack_bf16x2(acc[4], acc[5]), pack_bf16x2(acc[6], acc[7]));
+      }
+    }
+    if (!whole && tl == 0) {
+      KvPart p;
+      p.first = first;
+      p.end = end;
+      p.begin = at;
+      p.total = total;
+      p.b = b;
+      p.head = head;
+      p.tile = tile;
+      p.pad = 0;
+      a.parts[part] = p;
+    }
+    named_barrier(1 + gq, 128);  // the join buffer is free again
+    at = first + step1;
+  }
+}
+
+// Joins the items that several groups shared.  CTA (k, r): row r of the item that the
+// range of group k starts inside of, when group k holds the item's second part.
+template <class C>
+__global__ void __launch_bounds__(128) k_kv_join(const __grid_constant__ KvAttnArgs a, int workers) {
+  constexpr int D = C::D, ROWS = C::ROWS, V = D / 32;  // channels per lane
+  __shared__ float s_acc[4][D];
+  __shared__ float s_top[4], s_sum[4];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int k = static_cast<int>(blockIdx.x) + 1, r = blockIdx.y;
+  const KvPart p = a.parts[k * 2];
+  if (p.end == 0 || p.begin == p.first) return;  // nothing, or the group's range starts the item itself
+  // the group that holds step u is the largest g with g * total / workers <= u
+  auto group_of = [&](int64_t u) { return static_cast<int>(((u + 1) * workers - 1) / p.total); };
+  auto start_of = [&](int g) { return static_cast<int64_t>(g) * p.total / workers; };
+  const int g0 = group_of(p.first), last = group_of(p.end - 1);
+  if (p.begin != start_of(g0 + 1)) return;  // an earlier group's CTA joins this item
+  const KvSeq q = kv_seq(a.kb, p.b);
+  if (r >= q.n * a.group - p.tile * ROWS) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  // the first group's part is its range's start only when the item starts there
+  const int64_t head_part = static_cast<int64_t>(g0) * 2 + (start_of(g0) == p.first ? 0 : 1);
+  float top = -INFINITY, sum = 0.0f, acc[V] = {};
+  for (int g = g0 + w; g <= last; g += 4) {
+    if (start_of(g) >= start_of(g + 1)) continue;  // a group without steps
+    const int64_t part = g == g0 ? head_part : static_cast<int64_t>(g) * 2;
+    const float lse = a.part_lse[part * ROWS + r];
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 f = *reinterpret_cast<const float2 *>(a.part_o + (part * ROWS + r) * D + lane * V + i);
+      v[i] = f.x;
+      v[i + 1] = f.y;
+    }
+    const float next = fmaxf(top, lse);
+    const float f0 = top == -INFINITY ? 0.0f : ex2(top - next), f1 = lse == -INFINITY ? 0.0f : ex2(lse - next);
+    top = next;
+    sum = sum * f0 + f1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = acc[i] * f0 + v[i] * f1;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) s_acc[w][lane * V + i] = acc[i];
+  if (lane == 0) {
+    s_top[w] = top;
+    s_sum[w] = sum;
+  }
+  __syncthreads();
+  float all = s_top[0], total = 0.0f, f[4];
+#pragma unroll
+  for (int i = 1; i < 4; ++i) all = fmaxf(all, s_top[i]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = s_top[i] == -INFINITY && s_sum[i] == 0.0f ? 0.0f : ex2(s_top[i] - all);
+    total += f[i] * s_sum[i];
+  }
+  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+  const int rr = p.tile * ROWS + r, i = rr / a.group, h = rr - i * a.group;
+  uint16_t *dst = a.out + (static_cast<int64_t>(q.row0 + i) * a.heads * a.group + p.head * a.group + h) * D;
+  for (int c = threadIdx.x * 2; c < D; c += 256) {
+    float x = 0.0f, y = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x = fmaf(f[j], s_acc[j][c], x);
+      y = fmaf(f[j], s_acc[j][c + 1], y);
+    }
+    *reinterpret_cast<uint32_t *>(dst + c) = pack_bf16x2(x * inv, y * inv);
+  }
+}
+
+using Cfg64x1 = AttnCfg<64, 1, 4>;
+using Cfg64x2 = AttnCfg<64, 2, 4>;
+using Cfg128x1 = AttnCfg<128, 1, 4>;
+using Cfg128x2 = AttnCfg<128, 2, 3>;
+using Cfg256x1 = AttnCfg<256, 1, 3>;
+
+template <class C>
+cudaError_t run_attention(KvAttnArgs a, void *ws, int num_sms, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = smem_attr_once(reinterpret_cast<const void *>(k_kv_attention<C>), C::SMEM_BYTES, attr_done);
+  if (e != cudaSuccess) return e;
+  const int workers = num_sms * C::GROUPS;
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  a.parts = reinterpret_cast<KvPart *>(w);
+  w += static_cast<size_t>(workers) * 2 * sizeof(KvPart);
+  a.part_lse = reinterpret_cast<float *>(w);
+  w += static_cast<size_t>(workers) * 2 * C::ROWS * 4;
+  a.part_o = reinterpret_cast<float *>(w);
+  e = launch_k(k_kv_attention<C>, dim3(num_sms), dim3(C::THREADS), C::SMEM_BYTES, st, 1, a);
+  if (e != cudaSuccess) return e;
+  return launch_k(k_kv_join<C>, dim3(workers - 1, C::ROWS), dim3(128), 0, st, 1, a, workers);
+}
+
+template <class C>
+size_t workspace_of(int num_sms) {
+  return static_cast<size_t>(num_sms) * C::GROUPS * 2 * (sizeof(KvPart) + C::ROWS * 4 + C::ROWS * C::D * 4);
+}
+
+}  // namespace
+
+size_t kv_attention_workspace(int head_dim, int num_sms) {
+  switch (head_dim) {
+    case 64: return workspace_of<Cfg64x2>(num_sms);
+    case 128: return workspace_of<Cfg128x2>(num_sms);
+    default: return workspace_of<Cfg256x1>(num_sms);
+  }
+}
+
+cudaError_t launch_kv_attention(const qlora_kv_cache &c, const KvBatch &kb, const uint16_t *Q, int q_heads,
+                                int64_t q_token_stride, int64_t q_head_stride, float scale, int causal, int window,
+                                uint16_t *out, void *ws, const float levels[16], int num_sms, cudaStream_t st) {
+  KvAttnArgs a = {};
+  a.kb = kb;
+  a.Q = Q;
+  a.q_token_stride = q_token_stride;
+  a.q_head_stride = q_head_stride;
+  a.out = out;
+  a.k_codes = c.k_codes;
+  a.v_codes = c.v_codes;
+  a.k_absmax = c.k_absmax;
+  a.v_absmax = c.v_absmax;
+  a.heads = c.heads;
+  a.group = q_heads / c.heads;
+  // the grids whose levels are multiples of one value are stored as the (exact) multiples
+  const float unit = c.codebook == QLORA_CB_INT4 ? 7.0f : c.codebook == QLORA_CB_FP4_E2M1 ? 6.0f : 1.0f;
+  for (int i = 0; i < 16; ++i) {
+    float v = levels[i] * unit;
+    if (unit != 1.0f) v = static_cast<float>(static_cast<int>(v * 2.0f + (v < 0 ? -0.5f : 0.5f))) * 0.5f;
+    a.levels[i] = __float2half_rn(v);
+  }
+  a.scale_log2 = scale * 1.4426950408889634f / unit;
+  a.v_unit = 1.0f / unit;
+  a.causal = causal;
+  a.window = window;
+  // 16-row tiles once a sequence has on average more than 8 rows per key/value head (a
+  // tile's rows share the decoding of every key and value)
+  const bool wide = static_cast<int64_t>(kb.tokens) * a.group > 8 * static_cast<int64_t>(kb.batch);
+  switch (c.head_dim) {
+    case 64: return wide ? run_attention<Cfg64x2>(a, ws, num_sms, st) : run_attention<Cfg64x1>(a, ws, num_sms, st);
+    case 128: return wide ? run_attention<Cfg128x2>(a, ws, num_sms, st) : run_attention<Cfg128x1>(a, ws, num_sms, st);
+    default: return run_attention<Cfg256x1>(a, ws, num_sms, st);
+  }
+}
+
+}  // namespace qlora

@@ -14,8 +14,10 @@
  *     and gradients for L1, L2 only.
  * Around the layer: the optimiser step of the adapters (qlora_adamw_step),
  * merging a trained adapter into the quantised base and requantising
- * (qlora_merge_requantize), and the storage-format variants the pages compare
- * NF4 with (qlora_quantize_format and its companions).
+ * (qlora_merge_requantize), the storage-format variants the pages compare
+ * NF4 with (qlora_quantize_format and its companions), and, for serving, a
+ * key/value cache in the same 4-bit formats with the attention that reads it
+ * (qlora_kv_append, qlora_kv_read, qlora_kv_attention).
  *
  * Conventions of this library:
  *   W  [N, K]  frozen weight, bfloat16, row-major (out x in, as a framework
@@ -76,6 +78,7 @@ typedef enum {
 /* Bits OR-ed into *dev_err by kernels. */
 #define QLORA_DEVERR_NONFINITE 1   /* a weight to quantise (given, or merged) held Inf/NaN */
 #define QLORA_DEVERR_TIMEOUT   2   /* a pipeline wait exceeded its bound; outputs are undefined */
+#define QLORA_DEVERR_KV_INDEX  4   /* a qlora_kv_batch entry was out of range and was skipped (see there) */
 
 typedef struct qlora_nf4_weight {
   int64_t N, K;      /* logical shape of W */
@@ -360,6 +363,121 @@ qlora_status qlora_dequantize_format(const qlora_qweight *w, uint16_t *W_out, vo
  * (sums in float64; their order is unspecified).
  */
 qlora_status qlora_quant_error(const uint16_t *W, const uint16_t *W_hat, int64_t n, double *stats, void *stream);
+
+/* ------------------------------------------------------ 4-bit key/value cache
+ * (no counterpart on the pages: their block quantisation, applied to the keys
+ * and values of attention instead of a weight)
+ *
+ * A paged cache of keys and values: num_pages pages of page_size token slots,
+ * each slot holding `heads` keys and values of head_dim channels as 4-bit codes
+ * of one of the code books above, with one constant per block of 64 channels:
+ *   codes   [num_pages][heads][page_size][head_dim / 2] bytes (even channel in
+ *           the high nibble);
+ *   absmax  [num_pages][heads][page_size][head_dim / 64] bfloat16: the block's
+ *           largest magnitude, exact because the inputs are bfloat16.
+ * head_dim is 64, 128 or 256; page_size is 16, 32, 64, 128 or 256; heads
+ * <= 512.  The buffers are the caller's, on the device, 16-byte aligned.
+ */
+typedef struct qlora_kv_cache {
+  int64_t num_pages;
+  int page_size;
+  int heads;     /* key/value heads */
+  int head_dim;
+  int codebook;  /* QLORA_CB_* */
+  uint8_t *k_codes;
+  uint16_t *k_absmax;
+  uint8_t *v_codes;
+  uint16_t *v_absmax;
+} qlora_kv_cache;
+
+/*
+ * The sequences of one call, the same for all three operators.  Arrays are on
+ * the device, int32, 4-byte aligned.
+ *   token_start [batch + 1]  sequence b owns the call's token rows
+ *                            token_start[b] .. token_start[b+1] - 1 (n_b rows,
+ *                            0 allowed); ascending, within 0 .. tokens.
+ *   kv_len      [batch]      cached tokens of each sequence, the call's own
+ *                            included.  Row i of sequence b is its position
+ *                            kv_len[b] - n_b + i: the rows are its last n_b.
+ *   page_table  [batch][max_pages]  position p is slot p % page_size of page
+ *                            page_table[b][p / page_size]; entries past the
+ *                            sequence's last page are not read.
+ * `tokens` is the number of rows of the call's tensors; rows that no sequence
+ * owns (padding behind the last one) are neither read nor written.
+ * Values that only the device sees are checked there.  A token_start pair that
+ * descends or leaves 0 .. tokens, a kv_len outside 0 .. max_pages * page_size
+ * and a page outside 0 .. num_pages - 1 set QLORA_DEVERR_KV_INDEX and are
+ * clamped or skipped: no access leaves the buffers, and what belongs to that
+ * sequence is unspecified.
+ * batch <= QLORA_KV_MAX_BATCH; tokens <= 2^30, and so is kv_len.
+ */
+#define QLORA_KV_MAX_BATCH 4096
+typedef struct qlora_kv_batch {
+  int batch;
+  int max_pages;
+  int64_t tokens;
+  const int32_t *token_start;
+  const int32_t *kv_len;
+  const int32_t *page_table;
+} qlora_kv_batch;
+
+/* Byte sizes of the codes and of the absmax constants of the keys (the values
+ * take the same again). */
+qlora_status qlora_kv_cache_sizes(int64_t num_pages, int page_size, int heads, int head_dim, size_t *codes_bytes,
+                                  size_t *absmax_bytes);
+
+/*
+ * qlora_kv_append — quantise new keys and values into the cache.
+ * K, V: device bfloat16, element (row, head, channel) at row * token_stride +
+ * head * head_stride + channel (strides in elements, multiples of 8; 16-byte
+ * aligned): slices of a fused projection's output need no copy.
+ * Codes and constants of every block are those of qlora_quantize_format with
+ * blocks of 64 and QLORA_DQ_NONE: float32(x / absmax), nearest level, ties to
+ * the lower index, an all-zero block gives the first zero level.  A block
+ * holding Inf or NaN gets the constant NaN (it reads back as NaN) and sets
+ * QLORA_DEVERR_NONFINITE.  A row whose position is negative (kv_len < n_b) is
+ * skipped and sets QLORA_DEVERR_KV_INDEX.  Two rows of one call must not have
+ * the same page and slot (pages shared between sequences are for reading).
+ */
+qlora_status qlora_kv_append(const qlora_kv_cache *cache, const qlora_kv_batch *batch, const uint16_t *K,
+                             int64_t k_token_stride, int64_t k_head_stride, const uint16_t *V,
+                             int64_t v_token_stride, int64_t v_head_stride, int *dev_err, void *stream);
+
+/*
+ * qlora_kv_read — the stored keys and values of the same rows, dequantised:
+ * x_hat = bf16_rn(float32(level[code] * absmax)).  With n_b = kv_len[b] a whole
+ * sequence is read back.  K_out, V_out (each nullable): device bfloat16
+ * [tokens][heads][head_dim], 16-byte aligned.  Rows whose position is negative
+ * are left as they were and set QLORA_DEVERR_KV_INDEX.
+ */
+qlora_status qlora_kv_read(const qlora_kv_cache *cache, const qlora_kv_batch *batch, uint16_t *K_out,
+                           uint16_t *V_out, int *dev_err, void *stream);
+
+/* Workspace bytes of qlora_kv_attention (16-byte aligned, holds no state
+ * between calls; calls that may overlap need one each). */
+qlora_status qlora_kv_attention_workspace_size(const qlora_kv_cache *cache, int batch, int64_t tokens, int q_heads,
+                                               size_t *bytes);
+
+/*
+ * qlora_kv_attention — softmax attention of the call's rows over the cache.
+ *   out[row][h] = sum_j softmax_j(scale * q . k_j) v_j,  k = v = level * absmax
+ *                 (not rounded to bfloat16 in between)
+ * over the positions j < kv_len[b] that the row at position p sees: j <= p when
+ * causal != 0, and j > p - window when window > 0.  A row that sees nothing
+ * (an empty sequence, a negative position) gives zeros.
+ * Q: device bfloat16, strided like K above; q_heads is a multiple of `heads`
+ * (q_heads / heads <= 128, tokens * q_heads / heads <= 2^30), and query head h
+ * reads key/value head h / (q_heads / heads).  out: device bfloat16
+ * [tokens][q_heads][head_dim], 16-byte aligned, not overlapping Q.  The new
+ * tokens' own keys and values must have been appended before.  scale > 0.
+ * Scores, softmax statistics and sums are float32; identical inputs give
+ * identical bits.
+ * A non-finite stored constant or query makes the rows (and, for a value, the
+ * 64 channels) that see it NaN and no others.
+ */
+qlora_status qlora_kv_attention(const qlora_kv_cache *cache, const qlora_kv_batch *batch, const uint16_t *Q,
+                                int q_heads, int64_t q_token_stride, int64_t q_head_stride, float scale, int causal,
+                                int window, uint16_t *out, void *ws, size_t ws_bytes, int *dev_err, void *stream);
 
 /* Number of kernels this library has launched in this process so far. */
 uint64_t qlora_kernel_launch_count(void);

@@ -437,10 +437,13 @@ def qlora_adamw_step(tensors, lr: float, beta1: float = 0.9, beta2: float = 0.99
 
 
 # ---------------------------------------------------------------- 4-bit key/value cache
-def _here(t: torch.Tensor, name: str) -> None:
-    """The calls launch on the current device's stream: the tensors must be there."""
-    if t.device.index != torch.cuda.current_device():
-        raise QloraError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+# These run in every step of a decoding loop, so the checks read plain integers and
+# the descriptors of the C ABI are kept.
+def _kv_stream(device: int) -> int:
+    """The current stream of the cache's device, which must be the current device (the kernels launch there)."""
+    if torch._C._cuda_getDevice() != device:
+        raise QloraError(f"the cache is on cuda:{device}, the current device is cuda:{torch._C._cuda_getDevice()}")
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 @dataclass
@@ -472,6 +475,7 @@ class KVCache:
         self._c = _KVCache(self.num_pages, self.page_size, self.heads, self.head_dim, CODEBOOKS[self.codebook],
                            self.k_codes.data_ptr(), self.k_absmax.data_ptr(), self.v_codes.data_ptr(),
                            self.v_absmax.data_ptr())
+        self._device = self.k_codes.get_device()
 
     def nbytes(self) -> int:
         return 2 * (self.k_codes.numel() + 2 * self.k_absmax.numel())
@@ -505,29 +509,37 @@ class KVBatch:
         _need(self.page_table, torch.int32, (batch, max_pages), "page_table")
         if len({t.device for t in (self.token_start, self.kv_len, self.page_table)}) != 1:
             raise QloraError("KVBatch: the arrays are on different devices")
-        self._start, self._len, self._table = (t.data_ptr() for t in (self.token_start, self.kv_len, self.page_table))
         self.batch, self.max_pages = batch, max_pages
+        self._device = self.kv_len.get_device()
+        self._last = (-1, None)  # tokens and the descriptor made for them
 
     def c_struct(self, tokens: int) -> _KVBatch:
-        return _KVBatch(self.batch, self.max_pages, tokens, self._start, self._len, self._table)
+        known, c = self._last
+        if known != tokens:
+            c = _KVBatch(self.batch, self.max_pages, tokens, self.token_start.data_ptr(), self.kv_len.data_ptr(),
+                         self.page_table.data_ptr())
+            self._last = (tokens, c)
+        return c
 
 
-def _kv_devices(cache: KVCache, batch: KVBatch, **tensors) -> None:
-    _here(cache.k_codes, "cache")
-    _here(batch.kv_len, "batch")
-    for name, t in tensors.items():
-        if t is not None and t.device != cache.k_codes.device:
-            raise QloraError(f"{name} is on {t.device}, the cache on {cache.k_codes.device}")
+def _kv_devices(cache: KVCache, batch: KVBatch, *tensors) -> None:
+    d = cache._device
+    if batch._device != d:
+        raise QloraError(f"the batch is on cuda:{batch._device}, the cache on cuda:{d}")
+    for t in tensors:
+        if t is not None and t.get_device() != d:
+            raise QloraError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, the cache on cuda:{d}")
 
 
 def _kv_rows(t: torch.Tensor, heads, head_dim: int, name: str) -> tuple[int, int]:
     """A bfloat16 [tokens, heads, head_dim] tensor whose channels are contiguous (rows and heads may be
     strided); returns its row and head strides (0 for an axis of one element)."""
-    if (t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[2] != head_dim or t.stride(2) != 1
-            or (heads is not None and t.shape[1] != heads)):
+    shape, strides = t.shape, t.stride()
+    if (t.dtype != torch.bfloat16 or len(shape) != 3 or shape[2] != head_dim or strides[2] != 1
+            or (heads is not None and shape[1] != heads)):
         raise QloraError(f"{name}: expected bfloat16 [tokens, {heads if heads is not None else 'heads'}, {head_dim}] "
-                         f"with contiguous channels, got {t.dtype} {tuple(t.shape)} strides {t.stride()}")
-    return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+                         f"with contiguous channels, got {t.dtype} {tuple(shape)} strides {strides}")
+    return (strides[0] if shape[0] > 1 else 0, strides[1] if shape[1] > 1 else 0)
 
 
 def qlora_kv_append(cache: KVCache, batch: KVBatch, K: torch.Tensor, V: torch.Tensor,
@@ -538,11 +550,14 @@ def qlora_kv_append(cache: KVCache, batch: KVBatch, K: torch.Tensor, V: torch.Te
     vt, vh = _kv_rows(V, cache.heads, cache.head_dim, "V")
     if K.shape[0] != V.shape[0]:
         raise QloraError(f"K has {K.shape[0]} token rows, V {V.shape[0]}")
-    _kv_devices(cache, batch, K=K, V=V, dev_err=dev_err)
+    _kv_devices(cache, batch, K, V, dev_err)
+    stream = _kv_stream(cache._device)
     if K.shape[0] == 0:
         return
-    _check(lib().qlora_kv_append(cache._c, batch.c_struct(K.shape[0]), K.data_ptr(), kt, kh, V.data_ptr(), vt, vh,
-                                 _ptr(dev_err), _stream()), "qlora_kv_append")
+    st = lib().qlora_kv_append(cache._c, batch.c_struct(K.shape[0]), K.data_ptr(), kt, kh, V.data_ptr(), vt, vh,
+                               _ptr(dev_err), stream)
+    if st:
+        _check(st, "qlora_kv_append")
 
 
 def qlora_kv_read(cache: KVCache, batch: KVBatch, tokens: int, K_out: torch.Tensor | None = None,
@@ -554,14 +569,17 @@ def qlora_kv_read(cache: KVCache, batch: KVBatch, tokens: int, K_out: torch.Tens
     if K_out is None and V_out is None:
         K_out = torch.empty(shape, dtype=torch.bfloat16, device=cache.k_codes.device)
         V_out = torch.empty_like(K_out)
-    for t, name in ((K_out, "K_out"), (V_out, "V_out")):
-        if t is not None:
-            _need(t, torch.bfloat16, shape, name)
-    _kv_devices(cache, batch, K_out=K_out, V_out=V_out, dev_err=dev_err)
+    else:
+        for t, name in ((K_out, "K_out"), (V_out, "V_out")):
+            if t is not None:
+                _need(t, torch.bfloat16, shape, name)
+    _kv_devices(cache, batch, K_out, V_out, dev_err)
+    stream = _kv_stream(cache._device)
     if tokens == 0:
         return K_out, V_out
-    _check(lib().qlora_kv_read(cache._c, batch.c_struct(tokens), _ptr(K_out), _ptr(V_out), _ptr(dev_err),
-                               _stream()), "qlora_kv_read")
+    st = lib().qlora_kv_read(cache._c, batch.c_struct(tokens), _ptr(K_out), _ptr(V_out), _ptr(dev_err), stream)
+    if st:
+        _check(st, "qlora_kv_read")
     return K_out, V_out
 
 
@@ -581,20 +599,23 @@ def qlora_kv_attention(cache: KVCache, batch: KVBatch, Q: torch.Tensor, scale: f
     row to its last `window` positions.  Returns out, bfloat16
     [tokens, q_heads, head_dim] (zeros where a row sees nothing)."""
     qt, qh = _kv_rows(Q, None, cache.head_dim, "Q")
-    tokens, q_heads = Q.shape[0], Q.shape[1]
+    tokens, q_heads, dim = Q.shape
     if out is None:
-        out = torch.empty((tokens, q_heads, cache.head_dim), dtype=torch.bfloat16, device=Q.device)
-    _need(out, torch.bfloat16, (tokens, q_heads, cache.head_dim), "out")
+        out = torch.empty((tokens, q_heads, dim), dtype=torch.bfloat16, device=Q.device)
+    else:
+        _need(out, torch.bfloat16, (tokens, q_heads, dim), "out")
     if ws is None:
         need = qlora_kv_attention_workspace_size(cache, batch.batch, tokens, q_heads)
         ws = torch.empty(max(need, 16), dtype=torch.uint8, device=Q.device)
-    _kv_devices(cache, batch, Q=Q, out=out, ws=ws, dev_err=dev_err)
+    _kv_devices(cache, batch, Q, out, ws, dev_err)
+    stream = _kv_stream(cache._device)
     if tokens == 0:
         return out
-    _check(lib().qlora_kv_attention(cache._c, batch.c_struct(tokens), Q.data_ptr(), q_heads, qt, qh,
-                                    cache.head_dim ** -0.5 if scale is None else scale, int(causal),
-                                    window, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                    _ptr(dev_err), _stream()), "qlora_kv_attention")
+    st = lib().qlora_kv_attention(cache._c, batch.c_struct(tokens), Q.data_ptr(), q_heads, qt, qh,
+                                  dim ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
+                                  ws.data_ptr(), ws.nbytes, _ptr(dev_err), stream)
+    if st:
+        _check(st, "qlora_kv_attention")
     return out
 
 

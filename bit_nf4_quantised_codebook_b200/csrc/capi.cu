@@ -535,7 +535,8 @@ static qlora_status check_kv_shape(int64_t num_pages, int page_size, int heads, 
   if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128 && page_size != 256)
     return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (head_dim != 64 && head_dim != 128 && head_dim != 256) return QLORA_ERR_UNSUPPORTED_SHAPE;
-  if (heads > 512 || num_pages > (1ll << 30)) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (heads > 512 || num_pages > (1ll << 30) || num_pages * heads * page_size > (1ll << 31))
+    return QLORA_ERR_UNSUPPORTED_SHAPE;
   return QLORA_OK;
 }
 

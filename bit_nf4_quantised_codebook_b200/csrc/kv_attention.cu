@@ -21,11 +21,13 @@
 // Numbers.  Levels are held in fp16: exactly for the integer and float grids (stored as
 // the small integers they are multiples of), within 2^-12 for NF4.  Each query row is
 // scaled by a power of two to a largest magnitude in [2^13, 2^14) and is then exact in
-// fp16 down to 2^-38 of it.  Softmax weights enter the second product as
-// w = 2^(s + log2 cV - M_b + 6) in fp16 (within 2^-12), M_b being a running maximum of
-// s + log2 cV per row and block that lags by at most 8: what is below 2^-31 of the
-// largest contribution to a channel block is lost, whatever the constants' range.  The
-// running maximum and sum of the softmax itself and all accumulators are float32.
+// fp16 down to 2^-38 of it.  The softmax keeps a reference m per row (its running maximum
+// when last renewed) and float32 weights P = 2^(s - m) and their sum.  Into the second
+// product go w = P * cV * F_b in fp16 (within 2^-12), F_b a scale per row and block that
+// gives the largest contribution so far a w of 2^6 when last renewed.  m and F_b are renewed
+// when some w passes 2^14 or the sum 2^100, which after the first tokens is rare: the usual
+// step needs no maximum and no rescaling.  What is below 2^-31 of the largest contribution to
+// a block is lost, whatever the constants' range.  All accumulators are float32.
 //
 // Work.  An item is one sequence x row tile (8 * NT rows: tokens x the query heads of one
 // key/value head) x key/value head, cut into steps of 128 tokens.  The steps of all items
@@ -46,9 +48,10 @@ namespace qlora {
 namespace {
 
 constexpr int kStepTokens = 128;     // tokens of one step of a group (4 warps x 32)
-constexpr float kLag = 8.0f;         // a running maximum is renewed when passed by this much (log2)
-constexpr float kLift = 6.0f;        // weights are stored times 2^kLift
-constexpr float kFloor = -3.0e38f;   // "no maximum yet": finite, so that differences stay defined
+constexpr float kLift = 6.0f;          // a new largest contribution to a block gets the fp16 weight 2^kLift
+constexpr float kMostWeight = 16384.0f;  // a weight past this renews the scales
+constexpr float kMostSum = 0x1p100f;   // and so does a sum past this
+constexpr float kFloor = -3.0e38f;     // "no maximum yet": finite, so that differences stay defined
 
 struct KvAttnArgs {
   KvBatch kb;
@@ -113,7 +116,7 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
-// Loads of the cache: read once by this SM, so not kept in L1.
+// Loads of the cache, kept where they are written: early, ahead of their use.
 __device__ __forceinline__ uint2 ld_codes2(const uint8_t *p) {
   uint2 v;
   asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
@@ -126,17 +129,23 @@ __device__ __forceinline__ uint32_t ld_codes1(const uint8_t *p) {
 }
 template <int NB>
 __device__ __forceinline__ void ld_consts(const uint16_t *p, uint32_t (&c)[(NB + 1) / 2]) {
-  if (NB == 1) c[0] = __ldg(p);
-  if (NB == 2) c[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
-  if (NB == 4) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
-    c[0] = v.x;
-    c[(NB + 1) / 2 - 1] = v.y;
+  if (NB == 1) {
+    uint16_t v;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+    c[0] = v;
   }
+  if (NB == 2) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(c[0]) : "l"(p));
+  if (NB == 4) asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(c[0]), "=r"(c[(NB + 1) / 2 - 1]) : "l"(p));
 }
 template <int NB>
 __device__ __forceinline__ float const_of(const uint32_t (&c)[(NB + 1) / 2], int b) {
   return __uint_as_float(b & 1 ? c[b / 2] & 0xFFFF0000u : c[b / 2] << 16);
+}
+
+// log2 of the scale F of a block's weights, for the reference m and the largest
+// contribution mv.
+__device__ __forceinline__ float weight_exponent(float m, float mv) {
+  return fminf(fmaxf(kLift + (m - mv), -126.0f), 126.0f);
 }
 
 // Steps, row tiles and first token of a sequence's items.
@@ -165,7 +174,7 @@ struct AttnCfg {
   static constexpr int NB = D / 64;       // blocks of 64 channels
   static constexpr int GROUPS = GROUPS_;  // warp groups per CTA
   static constexpr int THREADS = GROUPS * 128;
-  static constexpr int T = D == 256 ? 1 : 2;  // tiles of 16 tokens loaded together
+  static constexpr int T = D * NT > 128 ? 1 : 2;  // tiles of 16 tokens loaded together
   static constexpr int CW = (NB + 1) / 2;     // words of a token's constants
   static constexpr int JOIN_FLOATS = 4 * ROWS * D;  // one group's four warps
   static constexpr int LSE_FLOATS = 4 * ROWS;
@@ -235,6 +244,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
   float *my_join = join + gq * (C::JOIN_FLOATS + C::LSE_FLOATS);
   float *my_lse = my_join + C::JOIN_FLOATS;
   const uint32_t tab = table | (lane * 4);
+  // this lane's place in a tile: keys of tokens g, g + 8, values of tokens 2t, 2t + 1, 2t + 8, 2t + 9
+  const uint8_t *lane_k = a.k_codes + g * (D / 2) + 8 * t, *lane_v = a.v_codes + 2 * t * (D / 2) + 4 * g;
+  const uint16_t *lane_kc = a.k_absmax + g * NB, *lane_vc = a.v_absmax + g * NB;
   if (gw == 0 && lane < 2) {  // no part yet
     a.parts[me * 2 + lane].end = 0;
     a.parts[me * 2 + lane].total = total;
@@ -323,7 +335,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     all_hi = __reduce_min_sync(0xFFFFFFFFu, all_hi);
 
     float o[NT][NB][4][4];
-    float l[NT][2], mx[NT][2], mv[NT][NB][2];
+    float l[NT][2], mx[NT][2];            // sum and reference of rows 2t, 2t + 1
+    float mv[NT][NB][2], fv[NT][NB][2];   // largest s + log2 cV when last renewed, and F = weight_scale(mx - mv)
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -331,7 +344,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
         l[n][c] = 0.0f;
         mx[n][c] = kFloor;
 #pragma unroll
-        for (int k = 0; k < NB; ++k) mv[n][k][c] = kFloor;
+        for (int k = 0; k < NB; ++k) {
+          mv[n][k][c] = kFloor;
+          fv[n][k][c] = 1.0f;
+        }
       }
 #pragma unroll
       for (int k = 0; k < NB; ++k)
@@ -344,10 +360,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     // ------------------------------------------------------------ the steps
     // This warp's 32-token chunks lie 128 apart; a chunk is worked off in 2 / T parts of T
     // tiles of 16 tokens.  The codes of the next part are loaded as soon as the registers of
-    // this one are free: keys after the first product, values after the second.
+    // this one are free: keys after the first product, values after the second.  A tile lies
+    // inside one page, so its 16 slots can be loaded whether or not the sequence ends among
+    // them; what lies past the end is masked like what a row does not see.
     constexpr int PARTS = 2 / T;
     const int units = (step1 - step0) * PARTS;
-    const int64_t page_rows_shift = a.kb.page_shift;
     uint2 kc[T][2][NB];
     uint32_t kcon[T][2][CW];
     uint32_t vc[T][4][NB];
@@ -355,74 +372,60 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     auto base_of = [&](int u) {
       return sp.lo + (step0 + u / PARTS) * kStepTokens + gw * 32 + (u % PARTS) * (T * 16);
     };
-    // flat cache row of token 0 of tile i, or -1 (a tile never crosses a page)
-    auto tile_row = [&](int tok) -> int64_t {
-      if (tok >= sp.q.len) return -1;
+    // cache row of a tile's first token; row 0 for tiles past the end and without a page
+    auto tile_row = [&](int tok) -> uint32_t {
+      if (tok >= sp.q.len) return 0;
       const int page = kv_page(a.kb, b, tok);
       if (page < 0) {
         kv_error(a.kb);
-        return -1;
+        return 0;
       }
-      return ((static_cast<int64_t>(page) * a.heads + head) << page_rows_shift) +
-             (tok & ((1 << a.kb.page_shift) - 1));
+      return ((static_cast<uint32_t>(page) * a.heads + head) << a.kb.page_shift) + (tok & ((1 << a.kb.page_shift) - 1));
     };
-    auto load_k = [&](int i, int tok, int64_t row) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const bool in = row >= 0 && tok + g + 8 * x < sp.q.len;
-        const int64_t rr = row + g + 8 * x;
-#pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          kc[i][x][k] = make_uint2(0, 0);
-          if (in) kc[i][x][k] = ld_codes2(a.k_codes + rr * (D / 2) + 32 * k + 8 * t);
-        }
-#pragma unroll
-        for (int k = 0; k < CW; ++k) kcon[i][x][k] = 0;
-        if (in) ld_consts<NB>(a.k_absmax + rr * NB, kcon[i][x]);
-      }
+    auto part_rows = [&](int tok, uint32_t (&row)[T]) {
+      row[0] = tile_row(tok);
+      // two tiles of one page unless pages are single tiles (or the second lies past the end: then any row does)
+      if (T == 2) row[T - 1] = a.kb.page_shift >= 5 ? row[0] + 16 : tile_row(tok + 16);
     };
-    auto load_v = [&](int i, int tok, int64_t row) {
+    auto load_k = [&](const uint32_t (&row)[T]) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int tt = 2 * t + (x & 1) + 8 * (x >> 1);
-        const bool in = row >= 0 && tok + tt < sp.q.len;
+      for (int i = 0; i < T; ++i) {
+        const uint8_t *p = lane_k + static_cast<uint64_t>(row[i]) * (D / 2);
+        const uint16_t *pc = lane_kc + static_cast<uint64_t>(row[i]) * NB;
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          vc[i][x][k] = 0;
-          if (in) vc[i][x][k] = ld_codes1(a.v_codes + (row + tt) * (D / 2) + 32 * k + 4 * g);
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int k = 0; k < NB; ++k) kc[i][x][k] = ld_codes2(p + x * 8 * (D / 2) + 32 * k);
+          ld_consts<NB>(pc + x * 8 * NB, kcon[i][x]);
         }
       }
+    };
+    auto load_v = [&](const uint32_t (&row)[T]) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const bool in = row >= 0 && tok + g + 8 * x < sp.q.len;
+      for (int i = 0; i < T; ++i) {
+        const uint8_t *p = lane_v + static_cast<uint64_t>(row[i]) * (D / 2);
+        const uint16_t *pc = lane_vc + static_cast<uint64_t>(row[i]) * NB;
 #pragma unroll
-        for (int k = 0; k < CW; ++k) vcon[i][x][k] = 0;
-        if (in) ld_consts<NB>(a.v_absmax + (row + g + 8 * x) * NB, vcon[i][x]);
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+          for (int k = 0; k < NB; ++k)
+            vc[i][x][k] = ld_codes1(p + ((x & 1) + 8 * (x >> 1)) * (D / 2) + 32 * k);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) ld_consts<NB>(pc + x * 8 * NB, vcon[i][x]);
       }
     };
-    int64_t row[T];
-#pragma unroll
-    for (int i = 0; i < T; ++i) {
-      const int tok = base_of(0) + 16 * i;
-      row[i] = tile_row(tok);
-      load_k(i, tok, row[i]);
-      load_v(i, tok, row[i]);
-    }
+    uint32_t row[T];
+    part_rows(base_of(0), row);
+    load_k(row);
+    load_v(row);
     for (int u = 0; u < units; ++u) {
       const int tok0 = base_of(u);
-      const int tok1 = base_of(u + 1);
       const bool more = u + 1 < units;
-      int64_t next[T];
-#pragma unroll
-      for (int i = 0; i < T; ++i) next[i] = more ? tile_row(tok1 + 16 * i) : -1;
-      // scores: s[i][n][0..3] = (token g, row 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1)
+      if (more) part_rows(base_of(u + 1), row);
+      // products of the scores: s[i][n][0..3] = (token g, row 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1)
       float s[T][NT][4];
 #pragma unroll
       for (int i = 0; i < T; ++i) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[i][n][c] = 0.0f;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
           float acc[NT][4];
@@ -457,27 +460,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
           }
           const float c0 = const_of<NB>(kcon[i][0], k), c1 = const_of<NB>(kcon[i][1], k);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            s[i][n][0] = fmaf(c0, acc[n][0], s[i][n][0]);
-            s[i][n][1] = fmaf(c0, acc[n][1], s[i][n][1]);
-            s[i][n][2] = fmaf(c1, acc[n][2], s[i][n][2]);
-            s[i][n][3] = fmaf(c1, acc[n][3], s[i][n][3]);
-          }
-        }
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          s[i][n][0] *= qs[n][0];
-          s[i][n][1] *= qs[n][1];
-          s[i][n][2] *= qs[n][0];
-          s[i][n][3] *= qs[n][1];
+            for (int c = 0; c < 4; ++c) {
+              const float cc = c < 2 ? c0 : c1;
+              s[i][n][c] = k == 0 ? cc * acc[n][c] : fmaf(cc, acc[n][c], s[i][n][c]);
+            }
         }
       }
-      if (more) {
+      if (more) load_k(row);
+      // scores, with what a row does not see at -inf: only where some row does not see the whole part
+      const bool masked = tok0 < all_lo || tok0 + T * 16 > all_hi;
 #pragma unroll
-        for (int i = 0; i < T; ++i) load_k(i, tok1 + 16 * i, next[i]);
-      }
-      // masks: only where some row does not see the whole part
-      if (tok0 < all_lo || tok0 + T * 16 > all_hi) {
+      for (int i = 0; i < T; ++i)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[i][n][c] *= qs[n][c & 1];
+      if (masked) {
 #pragma unroll
         for (int i = 0; i < T; ++i)
 #pragma unroll
@@ -488,32 +488,43 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
               if (j >= see_hi[n][c & 1] || j < see_lo[n][c & 1]) s[i][n][c] = -INFINITY;
             }
       }
-      // running maxima: of s, and of s + log2 cV for each block
-      float lv[T][2][NB];
+      // weights, in fp16 pairs (rows 2t, 2t + 1) for each block, and the new sums
+      uint32_t p[T][NT][NB][2];
+      float sum[NT][2];
+      auto weights = [&](bool hide) -> bool {
+        float most = 0.0f;
+        bool over = false;
 #pragma unroll
-      for (int i = 0; i < T; ++i)
+        for (int n = 0; n < NT; ++n) {
+          sum[n][0] = l[n][0];
+          sum[n][1] = l[n][1];
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
+          for (int i = 0; i < T; ++i)
 #pragma unroll
-          for (int k = 0; k < NB; ++k) lv[i][x][k] = lg2(const_of<NB>(vcon[i][x], k));
-      bool renew = false;
+            for (int x = 0; x < 2; ++x) {
+              const float s0 = s[i][n][2 * x], s1 = s[i][n][2 * x + 1];
+              const float p0 = ex2(s0 - mx[n][0]), p1 = ex2(s1 - mx[n][1]);
+              sum[n][0] += p0;
+              sum[n][1] += p1;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          float top = s[0][n][c];
-#pragma unroll
-          for (int i = 0; i < T; ++i) top = fmaxf(top, fmaxf(s[i][n][c], s[i][n][c + 2]));
-          renew |= top > mx[n][c] + kLag;
-#pragma unroll
-          for (int k = 0; k < NB; ++k) {
-            float tv = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < T; ++i) tv = fmaxf(tv, fmaxf(s[i][n][c] + lv[i][0][k], s[i][n][c + 2] + lv[i][1][k]));
-            renew |= tv > mv[n][k][c] + kLag;
-          }
+              for (int k = 0; k < NB; ++k) {
+                const float cv = const_of<NB>(vcon[i][x], k);
+                float w0 = p0 * (cv * fv[n][k][0]), w1 = p1 * (cv * fv[n][k][1]);
+                if (hide) {  // a token that a row does not see adds nothing, whatever its value's constant
+                  w0 = s0 == -INFINITY ? 0.0f : w0;
+                  w1 = s1 == -INFINITY ? 0.0f : w1;
+                }
+                most = fmaxf(most, fmaxf(w0, w1));
+                p[i][n][k][x] = pack_half2(w0, w1);
+              }
+            }
+          over |= sum[n][0] > kMostSum || sum[n][1] > kMostSum;
         }
-      if (__any_sync(0xFFFFFFFFu, renew)) {
+        return over || most > kMostWeight;
+      };
+      const bool over = masked ? weights(true) : weights(false);
+      if (__any_sync(0xFFFFFFFFu, over)) {
+        // renew: references to the maximum of the scores so far, scales to the largest contributions
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -523,17 +534,24 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
             for (int i = 0; i < T; ++i) top = fmaxf(top, fmaxf(s[i][n][c], s[i][n][c + 2]));
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-            l[n][c] *= ex2(mx[n][c] - top);
+            const float old = mx[n][c];
+            l[n][c] *= ex2(old - top);
             mx[n][c] = top;
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
               float tv = mv[n][k][c];
 #pragma unroll
-              for (int i = 0; i < T; ++i) tv = fmaxf(tv, fmaxf(s[i][n][c] + lv[i][0][k], s[i][n][c + 2] + lv[i][1][k]));
+              for (int i = 0; i < T; ++i)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                  tv = fmaxf(tv, s[i][n][c + 2 * x] + lg2(const_of<NB>(vcon[i][x], k)));
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) tv = fmaxf(tv, __shfl_xor_sync(0xFFFFFFFFu, tv, d));
-              const float f = ex2(mv[n][k][c] - tv);
+              // accumulated so far in units of 2^-(m + log2 F)
+              const float e = weight_exponent(top, tv);
+              const float f = ex2((old - top) + (e - weight_exponent(old, mv[n][k][c])));
               mv[n][k][c] = tv;
+              fv[n][k][c] = ex2(e);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 o[n][k][i][c] *= f;
@@ -541,29 +559,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
               }
             }
           }
+        weights(true);
       }
-      // weights and the second product
+      // the second product
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        l[n][0] = sum[n][0];
+        l[n][1] = sum[n][1];
+      }
 #pragma unroll
       for (int i = 0; i < T; ++i) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          l[n][0] += ex2(s[i][n][0] - mx[n][0]) + ex2(s[i][n][2] - mx[n][0]);
-          l[n][1] += ex2(s[i][n][1] - mx[n][1]) + ex2(s[i][n][3] - mx[n][1]);
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < NB; ++k) {
+            p[i][n][k][0] = movmatrix(p[i][n][k][0]);
+            p[i][n][k][1] = movmatrix(p[i][n][k][1]);
+          }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-          uint32_t p[NT][2];
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              // a token that a row does not see adds nothing, whatever its value's constant
-              const float s0 = s[i][n][2 * x], s1 = s[i][n][2 * x + 1], add = lv[i][x][k] + kLift;
-              const float w0 = s0 == -INFINITY ? 0.0f : ex2(s0 + add - mv[n][k][0]);
-              const float w1 = s1 == -INFINITY ? 0.0f : ex2(s1 + add - mv[n][k][1]);
-              p[n][x] = movmatrix(pack_half2(w0, w1));
-            }
-          }
           // even channels of tokens 2t, 2t + 1 in one byte (x), odd ones in another (y)
           const uint32_t v0 = vc[i][0][k], v1 = vc[i][1][k], v2 = vc[i][2][k], v3 = vc[i][3][k];
           const uint32_t x0 = (v0 & 0xF0F0F0F0u) | ((v1 >> 4) & 0x0F0F0F0Fu);
@@ -574,32 +588,29 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
             const uint32_t a0 = lookup<0>(x0, tab), a1 = lookup<0>(y0, tab), a2 = lookup<0>(x1, tab),
                            a3 = lookup<0>(y1, tab);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(o[n][k][0], a0, a1, a2, a3, p[n][0], p[n][1]);
+            for (int n = 0; n < NT; ++n) mma16816(o[n][k][0], a0, a1, a2, a3, p[i][n][k][0], p[i][n][k][1]);
           }
           {
             const uint32_t a0 = lookup<1>(x0, tab), a1 = lookup<1>(y0, tab), a2 = lookup<1>(x1, tab),
                            a3 = lookup<1>(y1, tab);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(o[n][k][1], a0, a1, a2, a3, p[n][0], p[n][1]);
+            for (int n = 0; n < NT; ++n) mma16816(o[n][k][1], a0, a1, a2, a3, p[i][n][k][0], p[i][n][k][1]);
           }
           {
             const uint32_t a0 = lookup<2>(x0, tab), a1 = lookup<2>(y0, tab), a2 = lookup<2>(x1, tab),
                            a3 = lookup<2>(y1, tab);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(o[n][k][2], a0, a1, a2, a3, p[n][0], p[n][1]);
+            for (int n = 0; n < NT; ++n) mma16816(o[n][k][2], a0, a1, a2, a3, p[i][n][k][0], p[i][n][k][1]);
           }
           {
             const uint32_t a0 = lookup<3>(x0, tab), a1 = lookup<3>(y0, tab), a2 = lookup<3>(x1, tab),
                            a3 = lookup<3>(y1, tab);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(o[n][k][3], a0, a1, a2, a3, p[n][0], p[n][1]);
+            for (int n = 0; n < NT; ++n) mma16816(o[n][k][3], a0, a1, a2, a3, p[i][n][k][0], p[i][n][k][1]);
           }
         }
       }
-      if (more) {
-#pragma unroll
-        for (int i = 0; i < T; ++i) load_v(i, tok1 + 16 * i, next[i]);
-      }
+      if (more) load_v(row);
     }
 
     // ------------------------------------------------------------ join the group's warps
@@ -615,9 +626,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
         if (g == 0) my_lse[gw * ROWS + r] = sum > 0.0f || sum != sum ? mx[n][c] + lg2(sum) : -INFINITY;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-          // channels 8g .. 8g + 7 of block k; M_b - m is at most log2 of the largest constant plus the lag
-          // (past float32's exponents when the constant is near its largest: applied as two halves)
-          const float f = mv[n][k][c] > kFloor ? ex2(0.5f * (mv[n][k][c] - mx[n][c] - kLift)) : 0.0f;
+          // channels 8g .. 8g + 7 of block k, without the weights' scale (a power of two that may
+          // pass float32's exponents: applied as two halves)
+          const float f = ex2(-0.5f * weight_exponent(mx[n][c], mv[n][k][c]));
           const float fi = f * inv;
           float *dst = my_join + (gw * ROWS + r) * D + 64 * k + 8 * g;
           *reinterpret_cast<float4 *>(dst) = make_float4(o[n][k][0][c] * fi * f, o[n][k][0][c + 2] * fi * f,
@@ -758,7 +769,7 @@ __global__ void __launch_bounds__(128) k_kv_join(const __grid_constant__ KvAttnA
 
 using Cfg64x1 = AttnCfg<64, 1, 4>;
 using Cfg64x2 = AttnCfg<64, 2, 4>;
-using Cfg128x1 = AttnCfg<128, 1, 4>;
+using Cfg128x1 = AttnCfg<128, 1, 3>;
 using Cfg128x2 = AttnCfg<128, 2, 3>;
 using Cfg256x1 = AttnCfg<256, 1, 3>;
 

@@ -376,7 +376,7 @@ qlora_status qlora_quant_error(const uint16_t *W, const uint16_t *W_hat, int64_t
  *   absmax  [num_pages][heads][page_size][head_dim / 64] bfloat16: the block's
  *           largest magnitude, exact because the inputs are bfloat16.
  * head_dim is 64, 128 or 256; page_size is 16, 32, 64, 128 or 256; heads
- * <= 512.  The buffers are the caller's, on the device, 16-byte aligned.
+ * <= 512; num_pages * heads * page_size <= 2^31.  The buffers are the caller's, on the device, 16-byte aligned.
  */
 typedef struct qlora_kv_cache {
   int64_t num_pages;

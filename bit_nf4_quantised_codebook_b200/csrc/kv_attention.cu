@@ -116,26 +116,24 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
-// Loads of the cache, kept where they are written: early, ahead of their use.
-__device__ __forceinline__ uint2 ld_codes2(const uint8_t *p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
+// 16 bytes from global to shared memory, past the first-level cache.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ uint32_t ld_codes1(const uint8_t *p) {
-  uint32_t v;
-  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
-  return v;
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the last N groups of this thread's copies have landed
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 template <int NB>
-__device__ __forceinline__ void ld_consts(const uint16_t *p, uint32_t (&c)[(NB + 1) / 2]) {
-  if (NB == 1) {
-    uint16_t v;
-    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
-    c[0] = v;
+__device__ __forceinline__ void ld_consts(const uint8_t *p, uint32_t (&c)[(NB + 1) / 2]) {
+  if (NB == 1) c[0] = *reinterpret_cast<const uint16_t *>(p);
+  if (NB == 2) c[0] = *reinterpret_cast<const uint32_t *>(p);
+  if (NB == 4) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    c[0] = v.x;
+    c[(NB + 1) / 2 - 1] = v.y;
   }
-  if (NB == 2) asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(c[0]) : "l"(p));
-  if (NB == 4) asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(c[0]), "=r"(c[(NB + 1) / 2 - 1]) : "l"(p));
 }
 template <int NB>
 __device__ __forceinline__ float const_of(const uint32_t (&c)[(NB + 1) / 2], int b) {
@@ -154,6 +152,7 @@ struct KvSpan {
   int tiles;   // row tiles per key/value head (0: no rows)
   int steps;   // steps of each item (at least 1 where there are rows)
   int lo;      // first cached token that a row may see, rounded down to 32
+  __device__ __forceinline__ int64_t units(int heads) const { return static_cast<int64_t>(tiles) * heads * steps; }
 };
 __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs &a, int b, int tile_rows) {
   KvSpan s;
@@ -174,23 +173,43 @@ struct AttnCfg {
   static constexpr int NB = D / 64;       // blocks of 64 channels
   static constexpr int GROUPS = GROUPS_;  // warp groups per CTA
   static constexpr int THREADS = GROUPS * 128;
-  static constexpr int T = D * NT > 128 ? 1 : 2;  // tiles of 16 tokens loaded together
+  static constexpr int T = D == 256 ? 1 : 2;  // tiles of 16 tokens in one part of a warp's work
+  static constexpr int PARTS = 2 / T;         // parts of a warp's 32 tokens of a step
   static constexpr int CW = (NB + 1) / 2;     // words of a token's constants
-  static constexpr int JOIN_FLOATS = 4 * ROWS * D;  // one group's four warps
-  static constexpr int LSE_FLOATS = 4 * ROWS;
-  static constexpr int SMEM_BYTES = 0x20000 + GROUPS * (JOIN_FLOATS + LSE_FLOATS) * 4;
+  // shared memory: a ring of parts per warp, the first FRONT of them before the table
+  static constexpr int CODES = T * 16 * (D / 2), CONSTS = T * 16 * NB * 2;  // bytes of a part's keys (values the same)
+  static constexpr int PART_BYTES = 2 * (CODES + CONSTS);
+  static constexpr int STAGES = D == 64 ? 4 : 2;
+  static constexpr int RING = STAGES * PART_BYTES;
+  static constexpr int WARPS = 4 * GROUPS;
+  static constexpr int FRONT = 7;
+  static constexpr int LSE_BYTES = WARPS * ROWS * 4;
+  static constexpr int SMEM_BYTES = 0x20000 + (WARPS - FRONT) * RING + LSE_BYTES + (THREADS + 1) * 8;
+  static_assert(ROWS * D * 4 <= RING, "a warp's outputs are joined in its ring");
+  static_assert(RING % 128 == 0 && FRONT * RING <= 0x10000 - 0x400, "rings before the table");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
 };
 
+// The token of a tile that index i < 8 of a product's token axis stands for (i + 8: 8 more).
+// A lane's value tokens, indices 2t and 2t + 1, are then t and 4 + (t ^ 2): with the swizzle
+// below, neither the key loads (lane (g, t): index g, 8 bytes) nor the value loads (lane
+// (g, t): indices 2t and 2t + 1, 4 bytes at 4g) of a warp meet in a bank.
+__device__ __forceinline__ int token_of(int i) { return i & 1 ? 4 + ((i >> 1) ^ 2) : i >> 1; }
+// 32-byte blocks of a token's codes are stored at block k ^ swizzle(token).
+template <int NB>
+__device__ __forceinline__ int swizzle(int token) {
+  return NB == 4 ? token & 3 : NB == 2 ? (token >> 1) & 1 : 0;
+}
+
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_constant__ KvAttnArgs a) {
-  constexpr int D = C::D, NT = C::NT, NB = C::NB, T = C::T, CW = C::CW, ROWS = C::ROWS;
+  constexpr int D = C::D, NT = C::NT, NB = C::NB, T = C::T, CW = C::CW, ROWS = C::ROWS, S = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t smem_base = smem_u32(smem);
   const uint32_t table = (smem_base + 0xFFFFu) & ~0xFFFFu;  // 64 KiB at a multiple of 64 KiB
-  // before the table: the line's prefix sums; after it: the groups' joins
-  int64_t *prefix = reinterpret_cast<int64_t *>(smem);
-  float *join = reinterpret_cast<float *>(smem + (table - smem_base) + 0x10000u);
+  uint8_t *tail = smem + (table - smem_base) + 0x10000u;    // rings, the joins' sums, the line's prefix sums
+  float *lse = reinterpret_cast<float *>(tail + (C::WARPS - C::FRONT) * C::RING);
+  int64_t *prefix = reinterpret_cast<int64_t *>(tail + (C::WARPS - C::FRONT) * C::RING + C::LSE_BYTES);
   __shared__ int64_t s_warp_sum[C::THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = warp >> 2, gw = warp & 3;  // group in the CTA, warp in the group
@@ -202,21 +221,19 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
   }
   pdl_wait();
   pdl_launch_dependents();
-  if (table - smem_base < (a.kb.batch + 1) * sizeof(int64_t)) {  // cannot happen while shared memory starts low
+  if (table - smem_base < C::FRONT * C::RING) {  // cannot happen while shared memory starts low
     if (tid < C::GROUPS * 2) a.parts[blockIdx.x * C::GROUPS * 2 + tid].end = 0;
     kv_error(a.kb);
     return;
   }
 
   // ---------------------------------------------------------------- the line of steps
+  // each thread sums a run of sequences; prefix[i] is where run i starts
+  const int run = (a.kb.batch + C::THREADS - 1) / C::THREADS;
   {
-    const int per = (a.kb.batch + C::THREADS - 1) / C::THREADS;
-    const int b0 = min(a.kb.batch, tid * per), b1 = min(a.kb.batch, b0 + per);
+    const int b0 = min(a.kb.batch, tid * run), b1 = min(a.kb.batch, b0 + run);
     int64_t sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      const KvSpan s = kv_span(a, b, ROWS);
-      sum += static_cast<int64_t>(s.tiles) * a.heads * s.steps;
-    }
+    for (int b = b0; b < b1; ++b) sum += kv_span(a, b, ROWS).units(a.heads);
     int64_t x = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -227,49 +244,64 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     __syncthreads();
     int64_t at = x - sum;
     for (int w = 0; w < warp; ++w) at += s_warp_sum[w];
-    for (int b = b0; b < b1; ++b) {
-      prefix[b] = at;
-      const KvSpan s = kv_span(a, b, ROWS);
-      at += static_cast<int64_t>(s.tiles) * a.heads * s.steps;
-    }
-    if (tid == C::THREADS - 1) prefix[a.kb.batch] = at;
+    prefix[tid] = at;
+    if (tid == C::THREADS - 1) prefix[C::THREADS] = at + sum;
     __syncthreads();
   }
-  const int64_t total = prefix[a.kb.batch];
+  const int64_t total = prefix[C::THREADS];
   const int64_t workers = static_cast<int64_t>(gridDim.x) * C::GROUPS;
   const int64_t me = static_cast<int64_t>(blockIdx.x) * C::GROUPS + gq;
   int64_t at = me * total / workers;
   const int64_t stop = (me + 1) * total / workers;
   const int64_t begin = at;
-  float *my_join = join + gq * (C::JOIN_FLOATS + C::LSE_FLOATS);
-  float *my_lse = my_join + C::JOIN_FLOATS;
   const uint32_t tab = table | (lane * 4);
-  // this lane's place in a tile: keys of tokens g, g + 8, values of tokens 2t, 2t + 1, 2t + 8, 2t + 9
-  const uint8_t *lane_k = a.k_codes + g * (D / 2) + 8 * t, *lane_v = a.v_codes + 2 * t * (D / 2) + 4 * g;
-  const uint16_t *lane_kc = a.k_absmax + g * NB, *lane_vc = a.v_absmax + g * NB;
+  auto ring_of = [&](int w) { return w < C::FRONT ? smem + w * C::RING : tail + (w - C::FRONT) * C::RING; };
+  uint8_t *ring = ring_of(warp);
+  // this lane's place in a part's codes: keys of index g and values of index 2t, by block
+  int koff[NB], voff[NB];
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+    koff[k] = token_of(g) * (D / 2) + 32 * (k ^ swizzle<NB>(token_of(g))) + 8 * t;
+    voff[k] = C::CODES + t * (D / 2) + 32 * (k ^ swizzle<NB>(t)) + 4 * g;
+  }
+  const int vodd = (4 + (t ^ 2) - t) * (D / 2);  // from index 2t to 2t + 1 (whose swizzle differs by NB / 2)
+  const int coff = 2 * C::CODES + token_of(g) * NB * 2;
+  // and in its copies: 16-byte chunk `lane` of each 512 bytes of codes, and one chunk of constants
+  constexpr int CH = D / 32;                 // chunks of a token
+  constexpr int CC = C::CONSTS / 16;         // chunks of a part's key constants
+  const int copy_dst = (lane / CH) * (D / 2) + (((lane % CH) ^ (swizzle<NB>(lane / CH) << 1)) << 4);
+  const uint16_t *const_src = (lane < CC ? a.k_absmax : a.v_absmax) + (lane % (2 * NB)) * 8;
+  const bool const_second = T == 2 && (lane % CC) >= CC / 2;  // of the part's second tile
+  const uint32_t ring_addr = smem_u32(ring);
   if (gw == 0 && lane < 2) {  // no part yet
     a.parts[me * 2 + lane].end = 0;
     a.parts[me * 2 + lane].total = total;
   }
 
   int b = 0;
-  if (at < stop) {  // last b with prefix[b] <= at (sequences without rows take no steps)
-    int lo = 0, hi = a.kb.batch;
+  int64_t seq_start = 0;
+  KvSpan sp = {};
+  if (at < stop) {
+    int lo = 0, hi = C::THREADS;  // last run that starts at or before `at` (empty ones follow the one that holds it)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (prefix[mid] <= at) lo = mid;
       else hi = mid;
     }
-    b = lo;
+    b = lo * run;
+    seq_start = prefix[lo];
+    sp = kv_span(a, b, ROWS);
   }
   while (at < stop) {
-    while (prefix[b + 1] <= at) ++b;
-    const KvSpan sp = kv_span(a, b, ROWS);
-    const int64_t rel = at - prefix[b];
+    while (seq_start + sp.units(a.heads) <= at) {  // on to the sequence that holds step `at`
+      seq_start += sp.units(a.heads);
+      sp = kv_span(a, ++b, ROWS);
+    }
+    const int64_t rel = at - seq_start;
     const int item = static_cast<int>(rel / sp.steps);
     const int step0 = static_cast<int>(rel - static_cast<int64_t>(item) * sp.steps);
     const int head = item % a.heads, tile = item / a.heads;
-    const int64_t first = prefix[b] + static_cast<int64_t>(item) * sp.steps, end = first + sp.steps;
+    const int64_t first = seq_start + static_cast<int64_t>(item) * sp.steps, end = first + sp.steps;
     const int step1 = stop < end ? static_cast<int>(stop - first) : sp.steps;
     const int row_limit = sp.q.n * a.group - tile * ROWS;  // rows of the tile that exist
 
@@ -358,74 +390,74 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     }
 
     // ------------------------------------------------------------ the steps
-    // This warp's 32-token chunks lie 128 apart; a chunk is worked off in 2 / T parts of T
-    // tiles of 16 tokens.  The codes of the next part are loaded as soon as the registers of
-    // this one are free: keys after the first product, values after the second.  A tile lies
-    // inside one page, so its 16 slots can be loaded whether or not the sequence ends among
-    // them; what lies past the end is masked like what a row does not see.
-    constexpr int PARTS = 2 / T;
-    const int units = (step1 - step0) * PARTS;
-    uint2 kc[T][2][NB];
-    uint32_t kcon[T][2][CW];
-    uint32_t vc[T][4][NB];
-    uint32_t vcon[T][2][CW];
+    // This warp's 32-token chunks lie 128 apart; a chunk is worked off in parts of T tiles of
+    // 16 tokens, copied STAGES - 1 parts ahead into this warp's ring.  A tile lies inside one
+    // page, so its 16 slots can be copied whether or not the sequence ends among them; what
+    // lies past the end is masked like what a row does not see.
+    const int units = (step1 - step0) * C::PARTS;
     auto base_of = [&](int u) {
-      return sp.lo + (step0 + u / PARTS) * kStepTokens + gw * 32 + (u % PARTS) * (T * 16);
+      return sp.lo + (step0 + u / C::PARTS) * kStepTokens + gw * 32 + (u % C::PARTS) * (T * 16);
     };
-    // cache row of a tile's first token; row 0 for tiles past the end and without a page
-    auto tile_row = [&](int tok) -> uint32_t {
-      if (tok >= sp.q.len) return 0;
-      const int page = kv_page(a.kb, b, tok);
-      if (page < 0) {
-        kv_error(a.kb);
-        return 0;
-      }
-      return ((static_cast<uint32_t>(page) * a.heads + head) << a.kb.page_shift) + (tok & ((1 << a.kb.page_shift) - 1));
+    // The page of each tile is loaded a part before it is used, and checked then.
+    const int32_t *pages = a.kb.page_table + static_cast<int64_t>(b) * a.kb.max_pages;
+    bool bad_page = false;
+    auto load_pages = [&](int u, int (&page)[T]) {
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+        page[i] = __ldg(pages + min((base_of(u) + 16 * i) >> a.kb.page_shift, a.kb.max_pages - 1));
     };
-    auto part_rows = [&](int tok, uint32_t (&row)[T]) {
-      row[0] = tile_row(tok);
-      // two tiles of one page unless pages are single tiles (or the second lies past the end: then any row does)
-      if (T == 2) row[T - 1] = a.kb.page_shift >= 5 ? row[0] + 16 : tile_row(tok + 16);
-    };
-    auto load_k = [&](const uint32_t (&row)[T]) {
+    auto copy_part = [&](int u, const int (&page)[T]) {
+      uint32_t row[T];  // cache row of each tile's first token; row 0 for tiles without a page
 #pragma unroll
       for (int i = 0; i < T; ++i) {
-        const uint8_t *p = lane_k + static_cast<uint64_t>(row[i]) * (D / 2);
-        const uint16_t *pc = lane_kc + static_cast<uint64_t>(row[i]) * NB;
+        const int tok = base_of(u) + 16 * i;
+        const bool bad = static_cast<unsigned>(page[i]) >= static_cast<unsigned>(a.kb.num_pages);
+        bad_page |= bad && tok < sp.q.len;
+        row[i] = bad ? 0
+                     : ((static_cast<uint32_t>(page[i]) * a.heads + head) << a.kb.page_shift) +
+                           (tok & ((1 << a.kb.page_shift) - 1));
+      }
+      const uint32_t dst = ring_addr + (u % S) * C::PART_BYTES;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+      for (int i = 0; i < T; ++i) {
+        const uint8_t *ks = a.k_codes + static_cast<uint64_t>(row[i]) * (D / 2) + lane * 16;
+        const uint8_t *vs = a.v_codes + static_cast<uint64_t>(row[i]) * (D / 2) + lane * 16;
 #pragma unroll
-          for (int k = 0; k < NB; ++k) kc[i][x][k] = ld_codes2(p + x * 8 * (D / 2) + 32 * k);
-          ld_consts<NB>(pc + x * 8 * NB, kcon[i][x]);
+        for (int j = 0; j < D / 64; ++j) {  // 512 bytes each
+          if (j * 512 + 512 <= 8 * D) {
+            copy16(dst + i * 8 * D + j * 512 + copy_dst, ks + j * 512);
+            copy16(dst + C::CODES + i * 8 * D + j * 512 + copy_dst, vs + j * 512);
+          }
         }
       }
+      if (lane < 2 * CC)
+        copy16(dst + 2 * C::CODES + lane * 16,
+               const_src + static_cast<uint64_t>(const_second ? row[T - 1] : row[0]) * NB);
     };
-    auto load_v = [&](const uint32_t (&row)[T]) {
+    int page[T];
+    {
+      int first_pages[S][T];
 #pragma unroll
-      for (int i = 0; i < T; ++i) {
-        const uint8_t *p = lane_v + static_cast<uint64_t>(row[i]) * (D / 2);
-        const uint16_t *pc = lane_vc + static_cast<uint64_t>(row[i]) * NB;
+      for (int j = 0; j < S; ++j) load_pages(j, first_pages[j]);
+      load_pages(S, page);
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-#pragma unroll
-          for (int k = 0; k < NB; ++k)
-            vc[i][x][k] = ld_codes1(p + ((x & 1) + 8 * (x >> 1)) * (D / 2) + 32 * k);
-#pragma unroll
-        for (int x = 0; x < 2; ++x) ld_consts<NB>(pc + x * 8 * NB, vcon[i][x]);
+      for (int j = 0; j < S; ++j) {
+        if (j < units) copy_part(j, first_pages[j]);
+        copies_commit();
       }
-    };
-    uint32_t row[T];
-    part_rows(base_of(0), row);
-    load_k(row);
-    load_v(row);
+    }
     for (int u = 0; u < units; ++u) {
       const int tok0 = base_of(u);
-      const bool more = u + 1 < units;
-      if (more) part_rows(base_of(u + 1), row);
+      copies_wait<S - 1>();
+      __syncwarp();  // every lane's copies of this part are there
+      const uint8_t *part = ring + (u % S) * C::PART_BYTES;
       // products of the scores: s[i][n][0..3] = (token g, row 2t), (g, 2t + 1), (g + 8, 2t), (g + 8, 2t + 1)
       float s[T][NT][4];
 #pragma unroll
       for (int i = 0; i < T; ++i) {
+        uint32_t kcon[2][CW];
+        ld_consts<NB>(part + coff + i * 32 * NB, kcon[0]);
+        ld_consts<NB>(part + coff + i * 32 * NB + 16 * NB, kcon[1]);
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
           float acc[NT][4];
@@ -433,7 +465,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c) acc[n][c] = 0.0f;
-          const uint2 w0 = kc[i][0][k], w1 = kc[i][1][k];
+          const uint2 w0 = *reinterpret_cast<const uint2 *>(part + i * 8 * D + koff[k]);
+          const uint2 w1 = *reinterpret_cast<const uint2 *>(part + i * 8 * D + 4 * D + koff[k]);
           {
             const uint32_t a0 = lookup<0>(w0.x, tab), a1 = lookup<0>(w1.x, tab), a2 = lookup<1>(w0.x, tab),
                            a3 = lookup<1>(w1.x, tab);
@@ -458,7 +491,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma16816(acc[n], a0, a1, a2, a3, q[n][k][3][0], q[n][k][3][1]);
           }
-          const float c0 = const_of<NB>(kcon[i][0], k), c1 = const_of<NB>(kcon[i][1], k);
+          const float c0 = const_of<NB>(kcon[0], k), c1 = const_of<NB>(kcon[1], k);
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -468,7 +501,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
             }
         }
       }
-      if (more) load_k(row);
+      uint32_t vcon[T][2][CW];
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+        ld_consts<NB>(part + coff + C::CONSTS + i * 32 * NB, vcon[i][0]);
+        ld_consts<NB>(part + coff + C::CONSTS + i * 32 * NB + 16 * NB, vcon[i][1]);
+      }
       // scores, with what a row does not see at -inf: only where some row does not see the whole part
       const bool masked = tok0 < all_lo || tok0 + T * 16 > all_hi;
 #pragma unroll
@@ -484,7 +522,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const int j = tok0 + 16 * i + g + 8 * (c >> 1);
+              const int j = tok0 + 16 * i + token_of(g) + 8 * (c >> 1);
               if (j >= see_hi[n][c & 1] || j < see_lo[n][c & 1]) s[i][n][c] = -INFINITY;
             }
       }
@@ -578,8 +616,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
           }
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-          // even channels of tokens 2t, 2t + 1 in one byte (x), odd ones in another (y)
-          const uint32_t v0 = vc[i][0][k], v1 = vc[i][1][k], v2 = vc[i][2][k], v3 = vc[i][3][k];
+          // even channels of indices 2t, 2t + 1 in one byte (x), odd ones in another (y)
+          auto word = [&](int offset) { return *reinterpret_cast<const uint32_t *>(part + i * 8 * D + offset); };
+          const uint32_t v0 = word(voff[k]), v1 = word(voff[k ^ (NB / 2)] + vodd);
+          const uint32_t v2 = word(voff[k] + 4 * D), v3 = word(voff[k ^ (NB / 2)] + 4 * D + vodd);
           const uint32_t x0 = (v0 & 0xF0F0F0F0u) | ((v1 >> 4) & 0x0F0F0F0Fu);
           const uint32_t y0 = ((v0 << 4) & 0xF0F0F0F0u) | (v1 & 0x0F0F0F0Fu);
           const uint32_t x1 = (v2 & 0xF0F0F0F0u) | ((v3 >> 4) & 0x0F0F0F0Fu);
@@ -610,8 +650,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
           }
         }
       }
-      if (more) load_v(row);
+      __syncwarp();  // every lane has read this part
+      if (u + S < units) copy_part(u + S, page);
+      copies_commit();
+      load_pages(u + S + 1, page);
     }
+    copies_wait<0>();
+    if (bad_page) kv_error(a.kb);
 
     // ------------------------------------------------------------ join the group's warps
 #pragma unroll
@@ -623,14 +668,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
         for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
         const int r = n * 8 + 2 * t + c;
         const float inv = sum > 0.0f || sum != sum ? a.v_unit / sum : 0.0f;
-        if (g == 0) my_lse[gw * ROWS + r] = sum > 0.0f || sum != sum ? mx[n][c] + lg2(sum) : -INFINITY;
+        if (g == 0) lse[warp * ROWS + r] = sum > 0.0f || sum != sum ? mx[n][c] + lg2(sum) : -INFINITY;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
           // channels 8g .. 8g + 7 of block k, without the weights' scale (a power of two that may
           // pass float32's exponents: applied as two halves)
           const float f = ex2(-0.5f * weight_exponent(mx[n][c], mv[n][k][c]));
           const float fi = f * inv;
-          float *dst = my_join + (gw * ROWS + r) * D + 64 * k + 8 * g;
+          float *dst = reinterpret_cast<float *>(ring) + r * D + 64 * k + 8 * g;
           *reinterpret_cast<float4 *>(dst) = make_float4(o[n][k][0][c] * fi * f, o[n][k][0][c + 2] * fi * f,
                                                          o[n][k][1][c] * fi * f, o[n][k][1][c + 2] * fi * f);
           *reinterpret_cast<float4 *>(dst + 4) = make_float4(o[n][k][2][c] * fi * f, o[n][k][2][c + 2] * fi * f,
@@ -638,6 +683,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
         }
       }
     named_barrier(1 + gq, 128);
+    const float *my_lse = lse + gq * 4 * ROWS;
     const bool whole = step0 == 0 && step1 == sp.steps;
     const int slot = at == begin ? 0 : 1;
     const int64_t part = me * 2 + slot;
@@ -650,11 +696,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
       float acc[8] = {};
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
-        const float lse = my_lse[w * ROWS + r];
-        const float f = lse == -INFINITY ? 0.0f : ex2(lse - top);
+        const float x = my_lse[w * ROWS + r];
+        const float f = x == -INFINITY ? 0.0f : ex2(x - top);
         wsum += f;
-        const float4 u = *reinterpret_cast<const float4 *>(my_join + (w * ROWS + r) * D + ch);
-        const float4 v = *reinterpret_cast<const float4 *>(my_join + (w * ROWS + r) * D + ch + 4);
+        const float *src = reinterpret_cast<const float *>(ring_of(gq * 4 + w)) + r * D + ch;
+        const float4 u = *reinterpret_cast<const float4 *>(src);
+        const float4 v = *reinterpret_cast<const float4 *>(src + 4);
         acc[0] = fmaf(f, u.x, acc[0]);
         acc[1] = fmaf(f, u.y, acc[1]);
         acc[2] = fmaf(f, u.z, acc[2]);
@@ -692,7 +739,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
       p.pad = 0;
       a.parts[part] = p;
     }
-    named_barrier(1 + gq, 128);  // the join buffer is free again
+    named_barrier(1 + gq, 128);  // the rings are free again
     at = first + step1;
   }
 }
@@ -769,7 +816,7 @@ __global__ void __launch_bounds__(128) k_kv_join(const __grid_constant__ KvAttnA
 
 using Cfg64x1 = AttnCfg<64, 1, 4>;
 using Cfg64x2 = AttnCfg<64, 2, 4>;
-using Cfg128x1 = AttnCfg<128, 1, 3>;
+using Cfg128x1 = AttnCfg<128, 1, 4>;
 using Cfg128x2 = AttnCfg<128, 2, 3>;
 using Cfg256x1 = AttnCfg<256, 1, 3>;
 

@@ -74,10 +74,11 @@ struct KvAttnArgs {
 // A group's part of an item that it shares with others (slot 0: the item its range
 // starts in; slot 1: the one it ends in).
 struct KvPart {
-  int64_t first, end;  // the item's steps on the line; end = 0: nothing here
-  int64_t begin;       // the group's first step of it
-  int64_t total;       // steps of the whole line
-  int b, head, tile, pad;
+  int present;
+  int b, head, tile;
+  int g0, last;   // the item's first and last group
+  int head_slot;  // slot of the first group's part
+  int joins;      // 1: the second part of its item, whose CTA joins them all
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -105,6 +106,13 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma16816_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
   pdl_wait();
   pdl_launch_dependents();
   if (table - smem_base < C::FRONT * C::RING) {  // cannot happen while shared memory starts low
-    if (tid < C::GROUPS * 2) a.parts[blockIdx.x * C::GROUPS * 2 + tid].end = 0;
+    if (tid < C::GROUPS * 2) a.parts[blockIdx.x * C::GROUPS * 2 + tid].joins = 0;
     kv_error(a.kb);
     return;
   }
@@ -274,8 +282,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
   const bool const_second = T == 2 && (lane % CC) >= CC / 2;  // of the part's second tile
   const uint32_t ring_addr = smem_u32(ring);
   if (gw == 0 && lane < 2) {  // no part yet
-    a.parts[me * 2 + lane].end = 0;
-    a.parts[me * 2 + lane].total = total;
+    a.parts[me * 2 + lane].present = 0;
+    a.parts[me * 2 + lane].joins = 0;
   }
 
   int b = 0;
@@ -461,17 +469,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
           float acc[NT][4];
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[n][c] = 0.0f;
           const uint2 w0 = *reinterpret_cast<const uint2 *>(part + i * 8 * D + koff[k]);
           const uint2 w1 = *reinterpret_cast<const uint2 *>(part + i * 8 * D + 4 * D + koff[k]);
           {
             const uint32_t a0 = lookup<0>(w0.x, tab), a1 = lookup<0>(w1.x, tab), a2 = lookup<1>(w0.x, tab),
                            a3 = lookup<1>(w1.x, tab);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma16816(acc[n], a0, a1, a2, a3, q[n][k][0][0], q[n][k][0][1]);
+            for (int n = 0; n < NT; ++n) mma16816_zero(acc[n], a0, a1, a2, a3, q[n][k][0][0], q[n][k][0][1]);
           }
           {
             const uint32_t a0 = lookup<2>(w0.x, tab), a1 = lookup<2>(w1.x, tab), a2 = lookup<3>(w0.x, tab),
@@ -728,15 +732,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
       }
     }
     if (!whole && tl == 0) {
+      // the group that holds step u is the largest g with g * total / workers <= u
+      auto group_of = [&](int64_t u) { return static_cast<int>(((u + 1) * workers - 1) / total); };
       KvPart p;
-      p.first = first;
-      p.end = end;
-      p.begin = at;
-      p.total = total;
+      p.present = 1;
       p.b = b;
       p.head = head;
       p.tile = tile;
-      p.pad = 0;
+      p.g0 = group_of(first);
+      p.last = group_of(end - 1);
+      p.head_slot = p.g0 * total / workers == first ? 0 : 1;
+      p.joins = at != first && at == (p.g0 + 1) * total / workers ? 1 : 0;
       a.parts[part] = p;
     }
     named_barrier(1 + gq, 128);  // the rings are free again
@@ -745,71 +751,83 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
 }
 
 // Joins the items that several groups shared.  CTA (k, r): row r of the item that the
-// range of group k starts inside of, when group k holds the item's second part.
+// range of group k starts inside of, when group k holds the item's second part.  The parts'
+// weights come first, all at once; then four warps add every fourth part each, eight loads in
+// flight, and their sums are added in order.
+constexpr int kMaxWorkers = 1024;
 template <class C>
-__global__ void __launch_bounds__(128) k_kv_join(const __grid_constant__ KvAttnArgs a, int workers) {
+__global__ void __launch_bounds__(128) k_kv_join(const __grid_constant__ KvAttnArgs a) {
   constexpr int D = C::D, ROWS = C::ROWS, V = D / 32;  // channels per lane
+  __shared__ float s_weight[kMaxWorkers];
   __shared__ float s_acc[4][D];
-  __shared__ float s_top[4], s_sum[4];
+  __shared__ float s_red[8];
   pdl_wait();
   pdl_launch_dependents();
   const int k = static_cast<int>(blockIdx.x) + 1, r = blockIdx.y;
   const KvPart p = a.parts[k * 2];
-  if (p.end == 0 || p.begin == p.first) return;  // nothing, or the group's range starts the item itself
-  // the group that holds step u is the largest g with g * total / workers <= u
-  auto group_of = [&](int64_t u) { return static_cast<int>(((u + 1) * workers - 1) / p.total); };
-  auto start_of = [&](int g) { return static_cast<int64_t>(g) * p.total / workers; };
-  const int g0 = group_of(p.first), last = group_of(p.end - 1);
-  if (p.begin != start_of(g0 + 1)) return;  // an earlier group's CTA joins this item
+  if (!p.joins) return;
   const KvSeq q = kv_seq(a.kb, p.b);
   if (r >= q.n * a.group - p.tile * ROWS) return;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  // the first group's part is its range's start only when the item starts there
-  const int64_t head_part = static_cast<int64_t>(g0) * 2 + (start_of(g0) == p.first ? 0 : 1);
-  float top = -INFINITY, sum = 0.0f, acc[V] = {};
-  for (int g = g0 + w; g <= last; g += 4) {
-    if (start_of(g) >= start_of(g + 1)) continue;  // a group without steps
-    const int64_t part = g == g0 ? head_part : static_cast<int64_t>(g) * 2;
-    const float lse = a.part_lse[part * ROWS + r];
-    float v[V];
-#pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const float2 f = *reinterpret_cast<const float2 *>(a.part_o + (part * ROWS + r) * D + lane * V + i);
-      v[i] = f.x;
-      v[i + 1] = f.y;
-    }
-    const float next = fmaxf(top, lse);
-    const float f0 = top == -INFINITY ? 0.0f : ex2(top - next), f1 = lse == -INFINITY ? 0.0f : ex2(lse - next);
-    top = next;
-    sum = sum * f0 + f1;
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = acc[i] * f0 + v[i] * f1;
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int n = p.last - p.g0 + 1;
+  auto part_of = [&](int i) { return static_cast<int64_t>(p.g0 + i) * 2 + (i == 0 ? p.head_slot : 0); };
+  float top = -INFINITY;
+  for (int i = tid; i < n; i += 128) {
+    const int64_t part = part_of(i);
+    const float lse = a.parts[part].present ? a.part_lse[part * ROWS + r] : -INFINITY;  // groups without steps
+    s_weight[i] = lse;
+    top = fmaxf(top, lse);
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) s_acc[w][lane * V + i] = acc[i];
-  if (lane == 0) {
-    s_top[w] = top;
-    s_sum[w] = sum;
-  }
+  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  if (lane == 0) s_red[w] = top;
   __syncthreads();
-  float all = s_top[0], total = 0.0f, f[4];
-#pragma unroll
-  for (int i = 1; i < 4; ++i) all = fmaxf(all, s_top[i]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = s_top[i] == -INFINITY && s_sum[i] == 0.0f ? 0.0f : ex2(s_top[i] - all);
-    total += f[i] * s_sum[i];
+  top = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+  float sum = 0.0f;
+  for (int i = tid; i < n; i += 128) {
+    const float lse = s_weight[i];
+    const float f = lse == -INFINITY ? 0.0f : ex2(lse - top);
+    s_weight[i] = f;
+    sum += f;
   }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  if (lane == 0) s_red[4 + w] = sum;
+  __syncthreads();
+  sum = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
+  float acc[V] = {};
+  auto add = [&](int i, const float2 (&v)[V / 2]) {
+    const float f = s_weight[i];
+    if (f == 0.0f) return;  // an absent part holds anything
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+      acc[j] = fmaf(f, v[j / 2].x, acc[j]);
+      acc[j + 1] = fmaf(f, v[j / 2].y, acc[j + 1]);
+    }
+  };
+  auto load = [&](int i, float2 (&v)[V / 2]) {
+    const float *src = a.part_o + (part_of(i) * ROWS + r) * D + lane * V;
+#pragma unroll
+    for (int j = 0; j < V / 2; ++j) v[j] = *reinterpret_cast<const float2 *>(src + 2 * j);
+  };
+  constexpr int U = 8;
+  for (int i0 = w; i0 < n; i0 += 4 * U) {
+    float2 v[U][V / 2];
+#pragma unroll
+    for (int j = 0; j < U; ++j) load(min(i0 + 4 * j, n - 1), v[j]);
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (i0 + 4 * j < n) add(i0 + 4 * j, v[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) s_acc[w][lane * V + j] = acc[j];
+  __syncthreads();
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   const int rr = p.tile * ROWS + r, i = rr / a.group, h = rr - i * a.group;
   uint16_t *dst = a.out + (static_cast<int64_t>(q.row0 + i) * a.heads * a.group + p.head * a.group + h) * D;
-  for (int c = threadIdx.x * 2; c < D; c += 256) {
-    float x = 0.0f, y = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x = fmaf(f[j], s_acc[j][c], x);
-      y = fmaf(f[j], s_acc[j][c + 1], y);
-    }
+  for (int c = tid * 2; c < D; c += 256) {
+    const float x = (s_acc[0][c] + s_acc[1][c]) + (s_acc[2][c] + s_acc[3][c]);
+    const float y = (s_acc[0][c + 1] + s_acc[1][c + 1]) + (s_acc[2][c + 1] + s_acc[3][c + 1]);
     *reinterpret_cast<uint32_t *>(dst + c) = pack_bf16x2(x * inv, y * inv);
   }
 }
@@ -825,6 +843,7 @@ cudaError_t run_attention(KvAttnArgs a, void *ws, int num_sms, cudaStream_t st) 
   static std::atomic<uint64_t> attr_done{0};
   cudaError_t e = smem_attr_once(reinterpret_cast<const void *>(k_kv_attention<C>), C::SMEM_BYTES, attr_done);
   if (e != cudaSuccess) return e;
+  if (num_sms * C::GROUPS > kMaxWorkers) num_sms = kMaxWorkers / C::GROUPS;
   const int workers = num_sms * C::GROUPS;
   uint8_t *w = static_cast<uint8_t *>(ws);
   a.parts = reinterpret_cast<KvPart *>(w);
@@ -834,7 +853,7 @@ cudaError_t run_attention(KvAttnArgs a, void *ws, int num_sms, cudaStream_t st) 
   a.part_o = reinterpret_cast<float *>(w);
   e = launch_k(k_kv_attention<C>, dim3(num_sms), dim3(C::THREADS), C::SMEM_BYTES, st, 1, a);
   if (e != cudaSuccess) return e;
-  return launch_k(k_kv_join<C>, dim3(workers - 1, C::ROWS), dim3(128), 0, st, 1, a, workers);
+  return launch_k(k_kv_join<C>, dim3(workers - 1, C::ROWS), dim3(128), 0, st, 1, a);
 }
 
 template <class C>

@@ -21,7 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqlora_nf4.so")
 SOURCES = ["codebook.cpp", "quantize.cu", "quantize_noalloc.cu", "linear.cu", "merge.cu", "formats.cu", "adamw.cu",
-           "kv_cache.cu", "kv_attention.cu", "selftest.cu",
+           "kv_cache.cu", "kv_attention.cu", "kv_prefill.cu", "selftest.cu",
            "capi.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 

@@ -616,7 +616,7 @@ qlora_status qlora_kv_attention_workspace_size(const qlora_kv_cache *cache, int 
   if (batch > QLORA_KV_MAX_BATCH || q_heads % cache->heads != 0 || q_heads / cache->heads > 128 ||
       tokens * (q_heads / cache->heads) > (1ll << 30))
     return QLORA_ERR_UNSUPPORTED_SHAPE;
-  *bytes = kv_attention_workspace(cache->head_dim, device_sms());
+  *bytes = kv_attention_workspace(cache->head_dim, q_heads / cache->heads, batch, tokens, device_sms());
   return QLORA_OK;
 }
 
@@ -644,7 +644,7 @@ qlora_status qlora_kv_attention(const qlora_kv_cache *cache, const qlora_kv_batc
   kv_levels(cache->codebook, levels);
   return cuda_status(launch_kv_attention(*cache, kv_device_batch(*cache, *batch, dev_err), Q, q_heads,
                                          q_token_stride, q_head_stride, scale, causal, std::min(window, 1 << 30), out,
-                                         ws, levels, device_sms(), static_cast<cudaStream_t>(stream)));
+                                         ws, levels, device_sms(), globals().timeout_ns, static_cast<cudaStream_t>(stream)));
 }
 
 uint64_t qlora_kernel_launch_count(void) { return g_launches.load(std::memory_order_relaxed); }

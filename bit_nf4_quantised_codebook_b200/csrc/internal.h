@@ -62,7 +62,7 @@ using AdamwTensor = qlora_adamw_tensor;
 constexpr int kAdamwMaxTensors = QLORA_ADAMW_MAX_TENSORS;
 cudaError_t launch_adamw(const AdamwTensor *t, int count, float lr, float b1, float b2, float eps, float wd,
                          double step_size, double bc2_sqrt, int num_sms, cudaStream_t st);
-// kv_cache.cu, kv_attention.cu
+// kv_cache.cu, kv_attention.cu, kv_prefill.cu
 struct KvBatch;  // kv_common.cuh
 KvBatch kv_device_batch(const qlora_kv_cache &c, const qlora_kv_batch &b, int *dev_err);
 bool build_kv_code_table(int codebook, uint32_t table[32]);
@@ -71,10 +71,11 @@ cudaError_t launch_kv_append(const qlora_kv_cache &c, const KvBatch &kb, const u
                              const uint32_t table[32], cudaStream_t st);
 cudaError_t launch_kv_read(const qlora_kv_cache &c, const KvBatch &kb, uint16_t *K_out, uint16_t *V_out,
                            const float levels[16], cudaStream_t st);
-size_t kv_attention_workspace(int head_dim, int num_sms);
+size_t kv_attention_workspace(int head_dim, int group, int batch, int64_t tokens, int num_sms);
 cudaError_t launch_kv_attention(const qlora_kv_cache &c, const KvBatch &kb, const uint16_t *Q, int q_heads,
                                 int64_t q_token_stride, int64_t q_head_stride, float scale, int causal, int window,
-                                uint16_t *out, void *ws, const float levels[16], int num_sms, cudaStream_t st);
+                                uint16_t *out, void *ws, const float levels[16], int num_sms,
+                                unsigned long long timeout_ns, cudaStream_t st);
 // selftest.cu
 cudaError_t launch_selftest_wait(unsigned long long timeout_ns, int *dev_err, int *gave_up, cudaStream_t st);
 

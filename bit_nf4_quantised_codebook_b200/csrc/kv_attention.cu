@@ -41,6 +41,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include "internal.h"
+#include "kv_attention.cuh"
 #include "kv_common.cuh"
 #include "launch.cuh"
 
@@ -48,59 +49,6 @@ namespace qlora {
 namespace {
 
 constexpr int kStepTokens = 128;     // tokens of one step of a group (4 warps x 32)
-constexpr float kLift = 6.0f;          // a new largest contribution to a block gets the fp16 weight 2^kLift
-constexpr float kMostWeight = 16384.0f;  // a weight past this renews the scales
-constexpr float kMostSum = 0x1p100f;   // and so does a sum past this
-constexpr float kFloor = -3.0e38f;     // "no maximum yet": finite, so that differences stay defined
-
-struct KvAttnArgs {
-  KvBatch kb;
-  const uint16_t *Q;
-  int64_t q_token_stride, q_head_stride;
-  uint16_t *out;
-  const uint8_t *k_codes, *v_codes;
-  const uint16_t *k_absmax, *v_absmax;
-  int heads, group;   // key/value heads; query heads of each
-  float scale_log2;   // scale * log2(e) / unit
-  float v_unit;       // 1 / unit: levels are stored times `unit`
-  int causal, window;
-  __half levels[16];
-  // workspace
-  float *part_o;      // [groups][2][8 * NT][D] normalised partial outputs
-  float *part_lse;    // [groups][2][8 * NT] log2 of their weights' sum
-  struct KvPart *parts;  // [groups][2]
-};
-
-// A group's part of an item that it shares with others (slot 0: the item its range
-// starts in; slot 1: the one it ends in).
-struct KvPart {
-  int present;
-  int b, head, tile;
-  int g0, last;   // the item's first and last group
-  int head_slot;  // slot of the first group's part
-  int joins;      // 1: the second part of its item, whose CTA joins them all
-};
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
-  uint32_t v;
-  asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
-// Table entry of byte I of w (lane address `tab`: table base | lane * 4).
-template <int I>
-__device__ __forceinline__ uint32_t lookup(uint32_t w, uint32_t tab) {
-  return lds32(prmt(w, tab, 0x7604u | (I << 4)));
-}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -118,20 +66,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-// 16 bytes from global to shared memory, past the first-level cache.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>  // all but the last N groups of this thread's copies have landed
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 template <int NB>
 __device__ __forceinline__ void ld_consts(const uint8_t *p, uint32_t (&c)[(NB + 1) / 2]) {
@@ -165,7 +99,8 @@ struct KvSpan {
 __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs &a, int b, int tile_rows) {
   KvSpan s;
   s.q = kv_seq(a.kb, b);
-  s.tiles = static_cast<int>((static_cast<int64_t>(s.q.n) * a.group + tile_rows - 1) / tile_rows);
+  const int rows = s.q.n * a.group;
+  s.tiles = rows > a.few_rows ? 0 : (rows + tile_rows - 1) / tile_rows;
   int lo = 0;
   if (a.window > 0) lo = max(0, min(s.q.len, s.q.pos0() - a.window + 1)) & ~31;
   s.lo = lo;
@@ -750,88 +685,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
   }
 }
 
-// Joins the items that several groups shared.  CTA (k, r): row r of the item that the
-// range of group k starts inside of, when group k holds the item's second part.  The parts'
-// weights come first, all at once; then four warps add every fourth part each, eight loads in
-// flight, and their sums are added in order.
-constexpr int kMaxWorkers = 1024;
-template <class C>
-__global__ void __launch_bounds__(128) k_kv_join(const __grid_constant__ KvAttnArgs a) {
-  constexpr int D = C::D, ROWS = C::ROWS, V = D / 32;  // channels per lane
-  __shared__ float s_weight[kMaxWorkers];
-  __shared__ float s_acc[4][D];
-  __shared__ float s_red[8];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int k = static_cast<int>(blockIdx.x) + 1, r = blockIdx.y;
-  const KvPart p = a.parts[k * 2];
-  if (!p.joins) return;
-  const KvSeq q = kv_seq(a.kb, p.b);
-  if (r >= q.n * a.group - p.tile * ROWS) return;
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  const int n = p.last - p.g0 + 1;
-  auto part_of = [&](int i) { return static_cast<int64_t>(p.g0 + i) * 2 + (i == 0 ? p.head_slot : 0); };
-  float top = -INFINITY;
-  for (int i = tid; i < n; i += 128) {
-    const int64_t part = part_of(i);
-    const float lse = a.parts[part].present ? a.part_lse[part * ROWS + r] : -INFINITY;  // groups without steps
-    s_weight[i] = lse;
-    top = fmaxf(top, lse);
-  }
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-  if (lane == 0) s_red[w] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-  float sum = 0.0f;
-  for (int i = tid; i < n; i += 128) {
-    const float lse = s_weight[i];
-    const float f = lse == -INFINITY ? 0.0f : ex2(lse - top);
-    s_weight[i] = f;
-    sum += f;
-  }
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-  if (lane == 0) s_red[4 + w] = sum;
-  __syncthreads();
-  sum = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
-  float acc[V] = {};
-  auto add = [&](int i, const float2 (&v)[V / 2]) {
-    const float f = s_weight[i];
-    if (f == 0.0f) return;  // an absent part holds anything
-#pragma unroll
-    for (int j = 0; j < V; j += 2) {
-      acc[j] = fmaf(f, v[j / 2].x, acc[j]);
-      acc[j + 1] = fmaf(f, v[j / 2].y, acc[j + 1]);
-    }
-  };
-  auto load = [&](int i, float2 (&v)[V / 2]) {
-    const float *src = a.part_o + (part_of(i) * ROWS + r) * D + lane * V;
-#pragma unroll
-    for (int j = 0; j < V / 2; ++j) v[j] = *reinterpret_cast<const float2 *>(src + 2 * j);
-  };
-  constexpr int U = 8;
-  for (int i0 = w; i0 < n; i0 += 4 * U) {
-    float2 v[U][V / 2];
-#pragma unroll
-    for (int j = 0; j < U; ++j) load(min(i0 + 4 * j, n - 1), v[j]);
-#pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (i0 + 4 * j < n) add(i0 + 4 * j, v[j]);
-  }
-#pragma unroll
-  for (int j = 0; j < V; ++j) s_acc[w][lane * V + j] = acc[j];
-  __syncthreads();
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int rr = p.tile * ROWS + r, i = rr / a.group, h = rr - i * a.group;
-  uint16_t *dst = a.out + (static_cast<int64_t>(q.row0 + i) * a.heads * a.group + p.head * a.group + h) * D;
-  for (int c = tid * 2; c < D; c += 256) {
-    const float x = (s_acc[0][c] + s_acc[1][c]) + (s_acc[2][c] + s_acc[3][c]);
-    const float y = (s_acc[0][c + 1] + s_acc[1][c + 1]) + (s_acc[2][c + 1] + s_acc[3][c + 1]);
-    *reinterpret_cast<uint32_t *>(dst + c) = pack_bf16x2(x * inv, y * inv);
-  }
-}
-
 using Cfg64x1 = AttnCfg<64, 1, 4>;
 using Cfg64x2 = AttnCfg<64, 2, 4>;
 using Cfg128x1 = AttnCfg<128, 1, 4>;
@@ -853,7 +706,7 @@ cudaError_t run_attention(KvAttnArgs a, void *ws, int num_sms, cudaStream_t st) 
   a.part_o = reinterpret_cast<float *>(w);
   e = launch_k(k_kv_attention<C>, dim3(num_sms), dim3(C::THREADS), C::SMEM_BYTES, st, 1, a);
   if (e != cudaSuccess) return e;
-  return launch_k(k_kv_join<C>, dim3(workers - 1, C::ROWS), dim3(128), 0, st, 1, a);
+  return launch_k(k_kv_join<C::D, C::ROWS, 1>, dim3(workers - 1, C::ROWS), dim3(128), 0, st, 1, a);
 }
 
 template <class C>
@@ -863,17 +716,29 @@ size_t workspace_of(int num_sms) {
 
 }  // namespace
 
-size_t kv_attention_workspace(int head_dim, int num_sms) {
+namespace {
+size_t few_workspace(int head_dim, int num_sms) {
   switch (head_dim) {
     case 64: return workspace_of<Cfg64x2>(num_sms);
     case 128: return workspace_of<Cfg128x2>(num_sms);
     default: return workspace_of<Cfg256x1>(num_sms);
   }
 }
+// Sequences with more rows (tokens x query heads per key/value head) than this go to the
+// many-row kernel.
+constexpr int kFewRows = 64;
+}  // namespace
+
+size_t kv_attention_workspace(int head_dim, int group, int batch, int64_t tokens, int num_sms) {
+  size_t bytes = (few_workspace(head_dim, num_sms) + 15) / 16 * 16;
+  if (tokens * group > kFewRows) bytes += kv_prefill_workspace(head_dim, group, batch, tokens, num_sms);
+  return bytes;
+}
 
 cudaError_t launch_kv_attention(const qlora_kv_cache &c, const KvBatch &kb, const uint16_t *Q, int q_heads,
                                 int64_t q_token_stride, int64_t q_head_stride, float scale, int causal, int window,
-                                uint16_t *out, void *ws, const float levels[16], int num_sms, cudaStream_t st) {
+                                uint16_t *out, void *ws, const float levels[16], int num_sms,
+                                unsigned long long timeout_ns, cudaStream_t st) {
   KvAttnArgs a = {};
   a.kb = kb;
   a.Q = Q;
@@ -897,6 +762,12 @@ cudaError_t launch_kv_attention(const qlora_kv_cache &c, const KvBatch &kb, cons
   a.v_unit = 1.0f / unit;
   a.causal = causal;
   a.window = window;
+  a.few_rows = kFewRows;
+  if (static_cast<int64_t>(kb.tokens) * a.group > kFewRows) {  // some sequence may have many rows
+    uint8_t *more = static_cast<uint8_t *>(ws) + (few_workspace(c.head_dim, num_sms) + 15) / 16 * 16;
+    const cudaError_t e = launch_kv_prefill(a, c.head_dim, more, num_sms, timeout_ns, st);
+    if (e != cudaSuccess) return e;
+  }
   // 16-row tiles once a sequence has on average more than 8 rows per key/value head (a
   // tile's rows share the decoding of every key and value)
   const bool wide = static_cast<int64_t>(kb.tokens) * a.group > 8 * static_cast<int64_t>(kb.batch);

@@ -1,0 +1,173 @@
+// kv_attention.cuh — what the two attention kernels over the 4-bit cache share: their
+// arguments, the table lookup that turns two codes into two fp16 levels, and the kernel
+// that joins the parts of an item (one sequence, key/value head and tile of query rows)
+// that several workers shared.
+#pragma once
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include "internal.h"
+#include "kv_common.cuh"
+#include "launch.cuh"
+
+namespace qlora {
+
+constexpr float kLift = 6.0f;          // a new largest contribution to a block gets the fp16 weight 2^kLift
+constexpr float kMostWeight = 16384.0f;  // a weight past this renews the scales
+constexpr float kMostSum = 0x1p100f;   // and so does a sum past this
+constexpr float kFloor = -3.0e38f;     // "no maximum yet": finite, so that differences stay defined
+
+struct KvAttnArgs {
+  KvBatch kb;
+  const uint16_t *Q;
+  int64_t q_token_stride, q_head_stride;
+  uint16_t *out;
+  const uint8_t *k_codes, *v_codes;
+  const uint16_t *k_absmax, *v_absmax;
+  int heads, group;   // key/value heads; query heads of each
+  float scale_log2;   // scale * log2(e) / unit
+  float v_unit;       // 1 / unit: levels are stored times `unit`
+  int causal, window;
+  int few_rows;       // sequences with more rows (tokens x group) than this go to the many-row kernel
+  __half levels[16];
+  // workspace
+  float *part_o;      // [workers][2][rows of a tile][D] normalised partial outputs
+  float *part_lse;    // [workers][2][rows of a tile] log2 of their weights' sum
+  struct KvPart *parts;  // [workers][2]
+};
+
+// A worker's part of an item that it shares with others (slot 0: the item its range
+// starts in; slot 1: the one it ends in).
+struct KvPart {
+  int present;
+  int b, head, tile;
+  int g0, last;   // the item's first and last worker
+  int head_slot;  // slot of the first worker's part
+  int joins;      // 1: the second part of its item, whose CTA joins them all
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+// Table entry of byte I of w (lane address `tab`: table base | lane * 4).
+template <int I>
+__device__ __forceinline__ uint32_t lookup(uint32_t w, uint32_t tab) {
+  return lds32(prmt(w, tab, 0x7604u | (I << 4)));
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// 16 bytes from global to shared memory, past the first-level cache.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // all but the last N groups of this thread's copies have landed
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Joins the items that several workers shared.  CTA (k, y): RPC rows of the item that the
+// range of worker k starts inside of, when worker k holds the item's second part.  The parts'
+// weights come first, all at once; then four warps add every fourth part each, eight loads in
+// flight, and their sums are added in order.
+constexpr int kMaxWorkers = 1024;
+template <int D, int ROWS, int RPC>
+__global__ void __launch_bounds__(128) k_kv_join(const __grid_constant__ KvAttnArgs a) {
+  constexpr int V = D / 32;  // channels per lane
+  __shared__ float s_weight[kMaxWorkers];
+  __shared__ float s_acc[4][D];
+  __shared__ float s_red[8];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int k = static_cast<int>(blockIdx.x) + 1;
+  const KvPart p = a.parts[k * 2];
+  if (!p.joins) return;
+  const KvSeq q = kv_seq(a.kb, p.b);
+  const int rows = min(q.n * a.group - p.tile * ROWS, (static_cast<int>(blockIdx.y) + 1) * RPC);
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int n = p.last - p.g0 + 1;
+  auto part_of = [&](int i) { return static_cast<int64_t>(p.g0 + i) * 2 + (i == 0 ? p.head_slot : 0); };
+  for (int r = blockIdx.y * RPC; r < rows; ++r) {
+    float top = -INFINITY;
+    for (int i = tid; i < n; i += 128) {
+      const int64_t part = part_of(i);
+      const float lse = a.parts[part].present ? a.part_lse[part * ROWS + r] : -INFINITY;  // workers without steps
+      s_weight[i] = lse;
+      top = fmaxf(top, lse);
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    if (lane == 0) s_red[w] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+    float sum = 0.0f;
+    for (int i = tid; i < n; i += 128) {
+      const float lse = s_weight[i];
+      const float f = lse == -INFINITY ? 0.0f : ex2(lse - top);
+      s_weight[i] = f;
+      sum += f;
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+    if (lane == 0) s_red[4 + w] = sum;
+    __syncthreads();
+    sum = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
+    float acc[V] = {};
+    auto add = [&](int i, const float2 (&v)[V / 2]) {
+      const float f = s_weight[i];
+      if (f == 0.0f) return;  // an absent part holds anything
+#pragma unroll
+      for (int j = 0; j < V; j += 2) {
+        acc[j] = fmaf(f, v[j / 2].x, acc[j]);
+        acc[j + 1] = fmaf(f, v[j / 2].y, acc[j + 1]);
+      }
+    };
+    auto load = [&](int i, float2 (&v)[V / 2]) {
+      const float *src = a.part_o + (part_of(i) * ROWS + r) * D + lane * V;
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) v[j] = *reinterpret_cast<const float2 *>(src + 2 * j);
+    };
+    constexpr int U = 8;
+    for (int i0 = w; i0 < n; i0 += 4 * U) {
+      float2 v[U][V / 2];
+#pragma unroll
+      for (int j = 0; j < U; ++j) load(min(i0 + 4 * j, n - 1), v[j]);
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (i0 + 4 * j < n) add(i0 + 4 * j, v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) s_acc[w][lane * V + j] = acc[j];
+    __syncthreads();
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int rr = p.tile * ROWS + r, i = rr / a.group, h = rr - i * a.group;
+    uint16_t *dst = a.out + (static_cast<int64_t>(q.row0 + i) * a.heads * a.group + p.head * a.group + h) * D;
+    for (int c = tid * 2; c < D; c += 256) {
+      const float x = (s_acc[0][c] + s_acc[1][c]) + (s_acc[2][c] + s_acc[3][c]);
+      const float y = (s_acc[0][c + 1] + s_acc[1][c + 1]) + (s_acc[2][c + 1] + s_acc[3][c + 1]);
+      *reinterpret_cast<uint32_t *>(dst + c) = pack_bf16x2(x * inv, y * inv);
+    }
+    if (RPC > 1) __syncthreads();  // the shared arrays are free again
+  }
+}
+
+// kv_prefill.cu
+size_t kv_prefill_workspace(int head_dim, int group, int batch, int64_t tokens, int num_sms);
+cudaError_t launch_kv_prefill(const KvAttnArgs &a, int head_dim, void *ws, int num_sms, unsigned long long timeout_ns,
+                              cudaStream_t st);
+
+}  // namespace qlora

@@ -1,0 +1,838 @@
+// kv_prefill.cu — attention over the 4-bit cache for sequences with many query rows
+// (prompt chunks): the same definition as kv_attention.cu, on the tensor cores of sm_100a.
+//
+// An item is one sequence x key/value head x tile of 256 query rows (tokens x the query
+// heads of that key/value head; 128 rows with 256 channels), cut into steps of 128 cached
+// tokens (64 with 256 channels).  The steps of all items form one line, cut evenly among
+// one CTA per SM; parts of items that CTAs share are joined by k_kv_join.
+//
+// A CTA's roles:
+//   warps 0-3, 4-7  softmax of 128 rows each, one row per thread, ping-pong: while one half
+//                   works on its scores the tensor cores serve the other
+//   warps 8-11      decode the step's keys and values from codes to fp16 in the 128-byte
+//                   swizzled operand layout: once for all 256 rows
+//   warp 12         one thread issues the MMAs
+// S = Q K^T (Q and K in shared memory) lands in TMEM; the softmax warps read it, replace it
+// in place by the weights P_b in fp16, one set per block of 64 channels, and P_b is the A
+// operand, from TMEM, of O_b += P_b V_b.  The values' constants multiply the weights, so
+// decoding a value is a table lookup and nothing else; the keys' constants multiply the
+// levels as fp16 numbers with at most 8 significant bits (times a power of two per token
+// that goes into the scores).
+//
+// Numbers: as in kv_attention.cu (levels and weights in fp16, everything else float32),
+// and one more rounding of level x constant to fp16 for the keys (2^-11).  Per row, weights
+// are 2^(s - r) * cV with one reference r for all blocks, renewed when some weight passes
+// 2^14 (then the largest contribution so far weighs 2^6 or more), so a block whose constants
+// are below 2^-20 of another block's loses bits.  Constants are taken relative to the
+// largest exponent among 32 tokens, so no range of constants overflows float32.
+//
+// Bound by: the shared-memory traffic of the MMAs' operands (A and B of Q K^T and B of P V
+// are read at 128 bytes per clock) and the issue slots of the softmax, about equally.
+#include <atomic>
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include "internal.h"
+#include "kv_attention.cuh"
+#include "kv_common.cuh"
+#include "launch.cuh"
+#include "ptx.cuh"
+
+namespace qlora {
+namespace {
+
+template <int D_>
+struct PreCfg {
+  static constexpr int D = D_;
+  static constexpr int NB = D / 64;               // blocks of 64 channels
+  static constexpr int MT = D == 256 ? 1 : 2;     // tiles of 128 rows
+  static constexpr int ROWS = 128 * MT;
+  static constexpr int N = D == 256 ? 64 : 128;   // cached tokens of a step
+  static constexpr int TW = N / 4;                // tokens of one decoding warp = columns of one softmax pass
+  static constexpr int Q_BYTES = 128 * D * 2;     // one row tile
+  static constexpr int KV_BYTES = N * D * 2;
+  static constexpr int P_COL = D == 256 ? 64 : 0; // where the weights go, from the scores' first column
+  static constexpr int SP_COLS = D == 256 ? 192 : 128;
+  static constexpr int O_COL = MT * SP_COLS;
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int THREADS = 13 * 32;
+  static constexpr int BARS = 15;
+  static constexpr int MISC_FLOATS = 2 * N + 2 * NB * N + 2 * 4;
+  static constexpr int MISC_BYTES = MISC_FLOATS * 4 + BARS * 8 + 32;
+  static constexpr int SMEM_BYTES = 0x20000 + KV_BYTES + MT * Q_BYTES;
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
+  static_assert(O_COL + MT * D <= TMEM_COLS, "TMEM columns");
+};
+
+constexpr unsigned long long kDrainNs = 1000000000ull;  // bound on the wait for the MMAs in flight at the end
+
+struct KvEntry {  // a row tile of a sequence; its heads follow one another on the line
+  int b, tile;
+  int lo;     // first cached token of its first step
+  int steps;  // at least 1
+};
+
+struct PrefillArgs {
+  KvAttnArgs a;
+  KvEntry *entries;
+  int64_t *prefix;  // [entries + 1]: where each entry's steps start on the line
+  int *count;       // entries
+  int max_entries;  // room for them
+  unsigned long long timeout_ns;
+};
+
+// Instruction descriptor, kind::f16: float32 accumulator, fp16 A and B.
+constexpr uint32_t idesc_f16(int m, int n, bool b_mn_major) {
+  return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(m >> 4) << 24);
+}
+
+// ---------------------------------------------------------------- the line of steps
+// One CTA lists the row tiles of the sequences that have many rows.
+constexpr int kPlanThreads = 1024;
+template <class C>
+__global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const __grid_constant__ PrefillArgs p) {
+  __shared__ int s_off[QLORA_KV_MAX_BATCH + 1];
+  __shared__ int64_t s_sum[kPlanThreads / 32];
+  const KvAttnArgs &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_launch_dependents();
+  // inclusive scan of one value per thread over the CTA
+  auto scan = [&](int64_t v) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v += y;
+    }
+    __syncthreads();  // s_sum is free
+    if (lane == 31) s_sum[warp] = v;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) v += s_sum[w];
+    return v;
+  };
+  const int run = (a.kb.batch + kPlanThreads - 1) / kPlanThreads;
+  const int b0 = min(a.kb.batch, tid * run), b1 = min(a.kb.batch, b0 + run);
+  int tiles[QLORA_KV_MAX_BATCH / kPlanThreads];
+  int64_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < QLORA_KV_MAX_BATCH / kPlanThreads; ++i) {
+    tiles[i] = 0;
+    if (b0 + i < b1) {
+      const int rows = kv_seq(a.kb, b0 + i).n * a.group;
+      if (rows > a.few_rows) tiles[i] = (rows + C::ROWS - 1) / C::ROWS;
+    }
+    sum += tiles[i];
+  }
+  const int64_t incl = scan(sum);
+  int off = static_cast<int>(incl - sum);
+#pragma unroll
+  for (int i = 0; i < QLORA_KV_MAX_BATCH / kPlanThreads; ++i) {
+    if (b0 + i < b1) s_off[b0 + i] = off;
+    off += tiles[i];
+  }
+  if (tid == kPlanThreads - 1) s_off[a.kb.batch] = static_cast<int>(incl);
+  __syncthreads();
+  // sequences that share rows (an error, reported where they are read) may list more than there is room for
+  const int count = min(s_off[a.kb.batch], p.max_entries);
+  if (count < s_off[a.kb.batch] && tid == 0) kv_error(a.kb);
+  int64_t carry = 0;
+  for (int base = 0; base < count; base += kPlanThreads) {
+    const int e = base + tid;
+    int64_t units = 0;
+    if (e < count) {
+      int lo = 0, hi = a.kb.batch;  // last b with s_off[b] <= e: the one with tiles among equals
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_off[mid] <= e) lo = mid;
+        else hi = mid;
+      }
+      const KvSeq q = kv_seq(a.kb, lo);
+      KvEntry t;
+      t.b = lo;
+      t.tile = e - s_off[lo];
+      const int i0 = t.tile * C::ROWS / a.group;
+      const int i1 = min(q.n - 1, (t.tile * C::ROWS + C::ROWS - 1) / a.group);
+      const int see = a.causal ? min(q.len, q.pos0() + i1 + 1) : q.len;
+      t.lo = a.window > 0 ? max(0, min(q.len, q.pos0() + i0 - a.window + 1)) & ~31 : 0;
+      t.steps = max(1, (see - t.lo + C::N - 1) / C::N);
+      p.entries[e] = t;
+      units = static_cast<int64_t>(t.steps) * a.heads;
+    }
+    const int64_t upto = scan(units);
+    if (e < count) p.prefix[e] = carry + upto - units;
+    __syncthreads();
+    for (int w = 0; w < kPlanThreads / 32; ++w) carry += s_sum[w];
+  }
+  if (tid == 0) {
+    p.prefix[count] = carry;
+    *p.count = count;
+  }
+}
+
+// ---------------------------------------------------------------- a worker's part of an item
+struct Segment {
+  int b, head, tile;
+  KvSeq q;
+  int lo;            // first cached token of step 0
+  int step0, step1;  // its steps
+  int rows;          // rows of the tile that exist (at most ROWS: the second half stays idle with one row tile)
+  bool whole;        // the item is this worker's alone
+  int slot;
+  int64_t first, end, at;  // the item's steps on the line, and where this part begins
+};
+
+template <class C>
+struct Line {
+  const PrefillArgs &p;
+  int64_t total, workers, me, begin, stop, at;
+  int e;
+  KvEntry t;
+  int64_t base, next_base;
+  __device__ __forceinline__ Line(const PrefillArgs &p_, int64_t total_, int e0)
+      : p(p_), total(total_), workers(gridDim.x), me(blockIdx.x), e(e0) {
+    begin = at = me * total / workers;
+    stop = (me + 1) * total / workers;
+    if (at < stop) load();
+  }
+  __device__ __forceinline__ void load() {
+    t = p.entries[e];
+    base = p.prefix[e];
+    next_base = p.prefix[e + 1];
+  }
+  __device__ __forceinline__ bool next(Segment &s) {
+    if (at >= stop) return false;
+    while (at >= next_base) {
+      ++e;
+      load();
+    }
+    const int64_t rel = at - base;
+    s.b = t.b;
+    s.tile = t.tile;
+    s.lo = t.lo;
+    s.head = static_cast<int>(rel / t.steps);
+    s.step0 = static_cast<int>(rel - static_cast<int64_t>(s.head) * t.steps);
+    s.first = base + static_cast<int64_t>(s.head) * t.steps;
+    s.end = s.first + t.steps;
+    s.step1 = stop < s.end ? static_cast<int>(stop - s.first) : t.steps;
+    s.whole = s.step0 == 0 && s.step1 == t.steps;
+    s.slot = at == begin ? 0 : 1;
+    s.at = at;
+    s.q = kv_seq(p.a.kb, s.b);
+    s.rows = min(s.q.n * p.a.group - s.tile * C::ROWS, C::ROWS);
+    at = s.first + s.step1;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&w)[4]) { ld_shared_v4(addr, w[0], w[1], w[2], w[3]); }
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_constant__ PrefillArgs p) {
+  constexpr int D = C::D, NB = C::NB, N = C::N, TW = C::TW, MT = C::MT;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const KvAttnArgs &a = p.a;
+  const uint32_t smem_base = smem_u32(smem);
+  const uint32_t table = (smem_base + 0xFFFFu) & ~0xFFFFu;  // 64 KiB at a multiple of 64 KiB
+  // before the table: keys, constants, barriers; in its gaps (the upper half of each 256
+  // bytes): two stages of codes; after it: values and queries
+  const uint32_t k_smem = (smem_base + 1023u) & ~1023u;
+  const uint32_t v_smem = table + 0x10000u, q_smem = v_smem + C::KV_BYTES;
+  float *cs = reinterpret_cast<float *>(smem + (k_smem - smem_base) + C::KV_BYTES);  // [2][N] score factors
+  float *cv = cs + 2 * N;                                                            // [2][NB][N] value constants
+  float *ec = cv + 2 * NB * N;                                                       // [2][4] their exponents
+  uint64_t *bars = reinterpret_cast<uint64_t *>(ec + 8);
+  uint64_t *kfull = bars, *kempty = bars + 1, *vfull = bars + 2, *vempty = bars + 3, *cfull = bars + 4,
+           *sfull = bars + 6, *pfull = bars + 8, *opv = bars + 10, *qfull = bars + 12, *drain = bars + 14;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::BARS);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  int *s_entry = reinterpret_cast<int *>(tmem_slot + 2);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (table - smem_base < C::KV_BYTES + 1024 + C::MISC_BYTES) {  // cannot happen while shared memory starts low
+    pdl_wait();
+    if (tid < 2) p.a.parts[blockIdx.x * 2 + tid].joins = 0;
+    kv_error(a.kb);
+    return;
+  }
+  if (tid == 0) {
+    mbar_init(kfull, 4);
+    mbar_init(kempty, 1);
+    mbar_init(vfull, 4);
+    mbar_init(vempty, 1);
+    mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&cfull[i], 4);
+      mbar_init(&sfull[i], 1);
+      mbar_init(&pfull[i], 128);
+      mbar_init(&opv[i], 1);
+      mbar_init(&qfull[i], 128);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 12) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  for (int i = tid; i < 256 * 32; i += C::THREADS) {
+    const int byte = i >> 5;
+    const __half2 h = __halves2half2(a.levels[byte >> 4], a.levels[byte & 15]);
+    *reinterpret_cast<__half2 *>(smem + (table - smem_base) + byte * 256 + (i & 31) * 4) = h;
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+  const int count = *p.count;
+  const int64_t total = p.prefix[count];
+  if (warp == 0) {  // the entry that holds this worker's first step: 32 probes at a time
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * total / gridDim.x;
+    int lo = 0, hi = count;
+    while (hi - lo > 1) {
+      const int stride = (hi - lo + 31) / 32;
+      const int probe = lo + lane * stride;
+      const unsigned below = __ballot_sync(0xFFFFFFFFu, probe < hi && p.prefix[min(probe, hi - 1)] <= at);
+      const int last = 31 - __clz(static_cast<int>(below));  // lane 0's probe is lo, at or below `at`
+      const int nlo = lo + last * stride;
+      hi = min(hi, nlo + stride);
+      lo = nlo;
+    }
+    if (lane == 0) *s_entry = lo;
+  }
+  if (tid == 0)
+    for (int i = 0; i < 2; ++i) {
+      a.parts[blockIdx.x * 2 + i].present = 0;
+      a.parts[blockIdx.x * 2 + i].joins = 0;
+    }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Line<C> line(p, total, *s_entry);
+  Segment sg;
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    return mbar_wait_bounded(bar, parity, abort_flag, a.kb.dev_err, p.timeout_ns);
+  };
+
+  if (warp < 8) {
+    // ================================================================ softmax: one row per thread
+    const int m = warp >> 2;
+    const int r = tid & 127;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_tmem = lanes + m * C::SP_COLS, p_tmem = s_tmem + C::P_COL, o_tmem = lanes + C::O_COL + m * D;
+    uint32_t steps_done = 0;  // of this row tile
+    uint32_t all_steps = 0;   // of the CTA
+    bool ok = true;
+    while (ok && line.next(sg)) {
+      const int nsteps = sg.step1 - sg.step0;
+      if (m * 128 >= sg.rows) {  // no row in this half
+        all_steps += nsteps;
+        continue;
+      }
+      // ---- the query row: scaled to fp16, into the swizzled operand
+      const int row = m * 128 + r;
+      const bool live = row < sg.rows;
+      const int rr = sg.tile * C::ROWS + row;
+      const int tok = live ? rr / a.group : 0, h = live ? rr - tok * a.group : 0;
+      float qs = 0.0f;
+      {
+        const uint16_t *src = a.Q + static_cast<int64_t>(sg.q.row0 + tok) * a.q_token_stride +
+                              static_cast<int64_t>(sg.head * a.group + h) * a.q_head_stride;
+        uint32_t mag = 0;
+        if (live) {
+#pragma unroll 8
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+            mag = __vmaxu2(__vmaxu2(mag, u.x & 0x7FFF7FFFu), u.y & 0x7FFF7FFFu);
+            mag = __vmaxu2(__vmaxu2(mag, u.z & 0x7FFF7FFFu), u.w & 0x7FFF7FFFu);
+          }
+        }
+        mag = max(mag >> 16, mag & 0xFFFFu);
+        int e = static_cast<int>(mag >> 7) - 127 - 13;  // largest magnitude in [2^13, 2^14)
+        if (mag == 0 || mag >= 0x7F80u) e = 0;
+        e = max(e, -120);
+        const float down = pow2(-e);
+        const uint32_t dst = q_smem + m * C::Q_BYTES + r * 128;
+#pragma unroll 8
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (live) u = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+          const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            o[i] = pack_half2(__uint_as_float(in[i] << 16) * down, __uint_as_float(in[i] & 0xFFFF0000u) * down);
+          st_shared_v4(dst + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+        }
+        qs = pow2(e) * a.scale_log2;
+        if (mag >= 0x7F80u) qs = __uint_as_float(0x7FC00000u);  // a non-finite query: its row is NaN throughout
+        fence_proxy_async_smem();
+        mbar_arrive(&qfull[m]);
+      }
+      const int pos = sg.q.pos0() + tok;
+      const int see_hi = !live ? 0x7FFFFFFF : a.causal ? min(sg.q.len, pos + 1) : sg.q.len;
+      const int see_lo = live && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+
+      float ref = kFloor, mx = kFloor, rv = kFloor, l = 0.0f;
+      for (int step = sg.step0; step < sg.step1; ++step, ++steps_done, ++all_steps) {
+        const int st = all_steps & 1;
+        const int tok0 = sg.lo + step * N;
+        ok = wait(&cfull[st], (all_steps >> 1) & 1) && wait(&sfull[m], steps_done & 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const bool hide = __any_sync(0xFFFFFFFFu, tok0 < see_lo || tok0 + N > see_hi);
+        const float *csr = cs + st * N, *cvr = cv + st * NB * N;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float s[TW];
+          {
+            uint32_t v[TW];
+            if constexpr (TW == 32) tmem_ld32(s_tmem + c * TW, v);
+            else tmem_ld16(s_tmem + c * TW, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < TW; j += 4) {
+              const float4 f = *reinterpret_cast<const float4 *>(csr + c * TW + j);
+              s[j] = __uint_as_float(v[j]) * f.x * qs;
+              s[j + 1] = __uint_as_float(v[j + 1]) * f.y * qs;
+              s[j + 2] = __uint_as_float(v[j + 2]) * f.z * qs;
+              s[j + 3] = __uint_as_float(v[j + 3]) * f.w * qs;
+            }
+          }
+          if (hide) {
+#pragma unroll
+            for (int j = 0; j < TW; ++j) {
+              const int t = tok0 + c * TW + j;
+              if (t >= see_hi || t < see_lo) s[j] = -INFINITY;
+            }
+          }
+          const float e_c = ec[st * 4 + c];
+          uint32_t w[NB * TW / 2];
+          float sum;
+          auto weights = [&](bool hidden) -> bool {
+            const float off = ref - e_c;
+            float most = 0.0f, sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+            for (int j = 0; j < TW; j += 4) {
+              float pw[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) pw[i] = ex2(s[j + i] - off);
+              sum0 += pw[0] + pw[2];
+              sum1 += pw[1] + pw[3];
+#pragma unroll
+              for (int k = 0; k < NB; ++k) {
+                const float4 f = *reinterpret_cast<const float4 *>(cvr + k * N + c * TW + j);
+                float x0 = pw[0] * f.x, x1 = pw[1] * f.y, x2 = pw[2] * f.z, x3 = pw[3] * f.w;
+                if (hidden) {  // a token that a row does not see adds nothing, whatever its value's constant
+                  x0 = s[j] == -INFINITY ? 0.0f : x0;
+                  x1 = s[j + 1] == -INFINITY ? 0.0f : x1;
+                  x2 = s[j + 2] == -INFINITY ? 0.0f : x2;
+                  x3 = s[j + 3] == -INFINITY ? 0.0f : x3;
+                }
+                most = fmaxf(most, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)));
+                w[k * (TW / 2) + j / 2] = pack_half2(x0, x1);
+                w[k * (TW / 2) + j / 2 + 1] = pack_half2(x2, x3);
+              }
+            }
+            sum = sum0 + sum1;
+            return most > kMostWeight || sum > kMostSum;
+          };
+          const bool over = hide ? weights(true) : weights(false);
+          if (__any_sync(0xFFFFFFFFu, over)) {
+            // renew the reference; what was accumulated and weighed so far follows
+            float top = mx;
+#pragma unroll
+            for (int j = 0; j < TW; ++j) {
+              top = fmaxf(top, s[j]);
+#pragma unroll
+              for (int k = 0; k < NB; ++k) rv = fmaxf(rv, s[j] + lg2(cvr[k * N + c * TW + j]) + e_c);
+            }
+            const float next = ceilf(fmaxf(rv - kLift, top + e_c - 100.0f));
+            const float f = next > ref ? ex2(ref - next) : 1.0f;  // a power of two
+            ref = fmaxf(ref, next);
+            l *= ex2(mx - top);
+            mx = top;
+            tmem_st_wait();
+            if (step > sg.step0) {
+#pragma unroll 1
+              for (int k = 0; k < D; k += 32) {
+                uint32_t v[32];
+                tmem_ld32(o_tmem + k, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
+                tmem_st32(o_tmem + k, v);
+              }
+            }
+            const __half2 f2 = __float2half2_rn(f);
+#pragma unroll 1
+            for (int k = 0; k < c; ++k) {
+              uint32_t v[NB * TW / 2];
+              if constexpr (NB == 1) tmem_ld16(p_tmem + k * 32, v);
+              else tmem_ld32(p_tmem + k * 32, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < NB * TW / 2; ++j) {
+                const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&v[j]), f2);
+                v[j] = *reinterpret_cast<const uint32_t *>(&x);
+              }
+              if constexpr (NB == 1) tmem_st16(p_tmem + k * 32, v);
+              else tmem_st32(p_tmem + k * 32, v);
+            }
+            tmem_st_wait();
+            weights(true);
+          }
+          l = fmaf(sum, ex2(ref - e_c - mx), l);
+          if constexpr (NB == 1) tmem_st16(p_tmem + c * 32, w);
+          else tmem_st32(p_tmem + c * 32, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&pfull[m]);
+      }
+      if (!ok) break;
+      // ---- the outputs of this part of the item
+      ok = wait(&opv[m], (steps_done - 1) & 1);
+      if (!__all_sync(0xFFFFFFFFu, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool any = l > 0.0f || l != l;
+      const float half_unit = ex2(0.5f * (ref - mx));  // applied twice: it may pass float32's exponents
+      const float inv = any ? a.v_unit / l * half_unit : 0.0f;
+      const int64_t part = static_cast<int64_t>(blockIdx.x) * 2 + sg.slot;
+      uint16_t *dst = a.out + ((static_cast<int64_t>(sg.q.row0 + tok) * a.heads + sg.head) * a.group + h) * D;
+      float *dst_part = a.part_o + (part * C::ROWS + row) * D;
+#pragma unroll 1
+      for (int k = 0; k < D; k += 32) {
+        uint32_t v[32];
+        tmem_ld32(o_tmem + k, v);
+        tmem_ld_wait();
+        if (live) {
+          float f[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(v[j]) * inv * half_unit;
+          if (sg.whole) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              *reinterpret_cast<uint4 *>(dst + k + j) =
+                  make_uint4(pack_bf16x2(f[j], f[j + 1]), pack_bf16x2(f[j + 2], f[j + 3]),
+                             pack_bf16x2(f[j + 4], f[j + 5]), pack_bf16x2(f[j + 6], f[j + 7]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4 *>(dst_part + k + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+          }
+        }
+      }
+      tc_fence_before();
+      if (!sg.whole) {
+        if (live) a.part_lse[part * C::ROWS + row] = any ? mx + lg2(l) : -INFINITY;
+        if (tid == 0) {
+          // the worker that holds step u is the largest g with g * total / workers <= u
+          auto worker_of = [&](int64_t u) { return static_cast<int>(((u + 1) * line.workers - 1) / total); };
+          KvPart kp;
+          kp.present = 1;
+          kp.b = sg.b;
+          kp.head = sg.head;
+          kp.tile = sg.tile;
+          kp.g0 = worker_of(sg.first);
+          kp.last = worker_of(sg.end - 1);
+          kp.head_slot = kp.g0 * total / line.workers == sg.first ? 0 : 1;
+          kp.joins = sg.at != sg.first && sg.at == (kp.g0 + 1) * total / line.workers ? 1 : 0;
+          a.parts[part] = kp;
+        }
+      }
+    }
+  } else if (warp < 12) {
+    // ================================================================ decoding: codes -> fp16 operands
+    const int dw = warp - 8;
+    constexpr int LPR = 32 / TW;                 // lanes per token
+    constexpr int PASSES = D / 32 / LPR;         // 16-byte pieces of codes per lane and side
+    const int sub = LPR == 2 ? lane & 1 : 0;
+    const int tr = dw * TW + lane / LPR;         // token of the step
+    const uint32_t tab = table | (lane * 4);
+    // raw codes of this warp's tokens, in the table's gaps: 128 bytes of every 256
+    auto gap = [&](int stage, int side, int off) {
+      return table + 128u + static_cast<uint32_t>(stage) * 32768u + static_cast<uint32_t>(side) * 16384u +
+             static_cast<uint32_t>((off >> 7) * 256 + (off & 127));
+    };
+    uint32_t n = 0;  // steps of the CTA so far
+    bool ok = true;
+    while (ok && line.next(sg)) {
+      const int32_t *pages = a.kb.page_table + static_cast<int64_t>(sg.b) * a.kb.max_pages;
+      bool bad_page = false;
+      constexpr int TILES = TW / 16;  // a warp's tokens in tiles of 16, each inside one page
+      auto load_pages = [&](int step, int (&page)[TILES]) {
+#pragma unroll
+        for (int i = 0; i < TILES; ++i)
+          page[i] = __ldg(pages + min((sg.lo + step * N + dw * TW + 16 * i) >> a.kb.page_shift, a.kb.max_pages - 1));
+      };
+      uint32_t kcon[NB], vcon[NB];  // constants of this lane's token, as loaded for the step to come
+      auto fetch = [&](int step, const int (&page)[TILES], int stage) {
+        uint32_t row[TILES];
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+          const int t = sg.lo + step * N + dw * TW + 16 * i;
+          const bool bad = static_cast<unsigned>(page[i]) >= static_cast<unsigned>(a.kb.num_pages);
+          bad_page |= bad && t < sg.q.len;
+          row[i] = bad ? 0
+                       : ((static_cast<uint32_t>(page[i]) * a.heads + sg.head) << a.kb.page_shift) +
+                             (t & ((1 << a.kb.page_shift) - 1));
+#pragma unroll
+          for (int x = 0; x < (8 * D + 511) / 512; ++x) {  // 8 D bytes of codes per tile and side
+            const int off = (dw * TW + 16 * i) * (D / 2) + x * 512 + lane * 16;
+            copy16(gap(stage, 0, off), a.k_codes + static_cast<uint64_t>(row[i]) * (D / 2) + x * 512 + lane * 16);
+            copy16(gap(stage, 1, off), a.v_codes + static_cast<uint64_t>(row[i]) * (D / 2) + x * 512 + lane * 16);
+          }
+        }
+        copies_commit();
+        const int in_warp = lane / LPR;
+        const uint64_t crow = static_cast<uint64_t>(row[TILES == 2 ? in_warp >> 4 : 0]) + (in_warp & 15);
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          kcon[k] = __ldg(a.k_absmax + crow * NB + k);
+          vcon[k] = __ldg(a.v_absmax + crow * NB + k);
+        }
+      };
+      int page[TILES];
+      load_pages(sg.step0, page);
+      fetch(sg.step0, page, n & 1);
+      load_pages(sg.step0 + 1, page);
+      for (int step = sg.step0; step < sg.step1; ++step, ++n) {
+        const int st = n & 1;
+        uint32_t kb[NB], vb[NB];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          kb[k] = kcon[k];
+          vb[k] = vcon[k];
+        }
+        if (step + 1 < sg.step1) {
+          fetch(step + 1, page, st ^ 1);
+          load_pages(step + 2, page);
+          copies_wait<1>();
+        } else {
+          copies_wait<0>();
+        }
+        __syncwarp();
+        if (n > 0) ok = wait(kempty, (n - 1) & 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        // ---- constants: keys as fp16 below 2^12 and a power of two per token, values relative
+        // to the warp's largest exponent
+        uint32_t kmax = 0, vmax = 0;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          kmax = max(kmax, kb[k]);
+          vmax = max(vmax, vb[k] < 0x7F80u ? vb[k] : 0u);
+        }
+        const int ke = max(static_cast<int>(kmax >> 7) - 127, -110);
+        const bool kbad = kmax >= 0x7F80u;
+        const float kdown = kbad ? 0.0f : pow2(11 - ke);
+        __half2 kc[NB];
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+          kc[k] = kbad ? __float2half2_rn(0.0f) : __float2half2_rn(__uint_as_float(kb[k] << 16) * kdown);
+        vmax = __reduce_max_sync(0xFFFFFFFFu, vmax);
+        const int ve = min(max(static_cast<int>(vmax >> 7) - 127, -100), 126);
+        if (sub == 0) {
+          cs[st * N + tr] = kbad ? __uint_as_float(0x7FC00000u) : pow2(ke - 11);
+#pragma unroll
+          for (int k = 0; k < NB; ++k)
+            cv[(st * NB + k) * N + tr] =
+                vb[k] >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __uint_as_float(vb[k] << 16) * pow2(-ve);
+        }
+        if (lane == 0) ec[st * 4 + dw] = static_cast<float>(ve);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cfull[st]);
+        // ---- codes of this lane's token: 16 bytes (32 channels) at a time, in an order that
+        // keeps eight neighbouring lanes out of each other's banks
+        auto decode = [&](int side, uint32_t dst, auto scale) {
+#pragma unroll
+          for (int it = 0; it < PASSES; ++it) {
+            const int q = NB == 1 ? it ^ ((tr >> 2) & 1) : NB == 2 ? it ^ ((tr >> 1) & 3) : 4 * sub + (it ^ (tr & 3));
+            uint32_t w[4];
+            lds128(gap(st, side, tr * (D / 2) + q * 16), w);
+            const uint32_t out = dst + (q >> 1) * (N * 128) + tr * 128;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t o[4] = {lookup<0>(w[j], tab), lookup<1>(w[j], tab), lookup<2>(w[j], tab), lookup<3>(w[j], tab)};
+              scale(o, q >> 1);
+              st_shared_v4(out + ((((q & 1) * 4 + j) ^ (tr & 7)) << 4), o[0], o[1], o[2], o[3]);
+            }
+          }
+        };
+        decode(0, k_smem, [&](uint32_t (&o)[4], int blk) {
+          __half2 c = kc[0];
+#pragma unroll
+          for (int k = 1; k < NB; ++k)
+            if (blk == k) c = kc[k];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&o[i]), c);
+            o[i] = *reinterpret_cast<const uint32_t *>(&x);
+          }
+        });
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kfull);
+        if (n > 0) ok = wait(vempty, (n - 1) & 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        decode(1, v_smem, [](uint32_t (&)[4], int) {});
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(vfull);
+      }
+      copies_wait<0>();
+      __syncwarp();
+      if (bad_page) kv_error(a.kb);
+    }
+  } else if (lane == 0) {
+    // ================================================================ MMA issue
+    constexpr uint32_t idesc_s = idesc_f16(128, N, false), idesc_o = idesc_f16(128, 64, true);
+    uint32_t n = 0;                 // steps of the CTA
+    uint32_t done[2] = {0, 0};      // P V products of each row tile
+    uint32_t queries[2] = {0, 0};
+    bool ok = true;
+    auto scores = [&](int m) {  // S_m = Q_m K^T
+      const uint32_t d = tmem + m * C::SP_COLS;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint64_t ad = smem_desc_sw128(q_smem + m * C::Q_BYTES + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024);
+        const uint64_t bd = smem_desc_sw128(k_smem + (k >> 2) * (N * 128) + (k & 3) * 32, 16, 1024);
+        mma_bf16_ss(d, ad, bd, idesc_s, k > 0 ? 1u : 0u);
+      }
+    };
+    auto outputs = [&](int m, bool first) {  // O_m,b += P_m,b V_b
+      const uint32_t pt = tmem + m * C::SP_COLS + C::P_COL, d = tmem + C::O_COL + m * D;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int k = 0; k < N / 16; ++k) {
+          const uint32_t at = TW == 32 ? 32 * (k >> 1) + 16 * b + 8 * (k & 1) : 32 * k + 8 * b;
+          const uint64_t bd = smem_desc_sw128(v_smem + b * (N * 128) + k * 2048, 8192, 1024);
+          mma_bf16_ts(d + 64 * b, pt + at, bd, idesc_o, !first || k > 0 ? 1u : 0u);
+        }
+    };
+    while (ok && line.next(sg)) {
+      const int tiles = MT == 2 && sg.rows > 128 ? 2 : 1;
+      const int nsteps = sg.step1 - sg.step0;
+      for (int m = 0; m < tiles && ok; ++m) ok = wait(&qfull[m], queries[m]++ & 1);
+      if (ok) ok = wait(kfull, n & 1);
+      if (!ok) break;
+      tc_fence_after();
+      // the previous item's outputs have been waited for by its softmax warps, which then
+      // announced these queries
+      for (int m = 0; m < tiles; ++m) {
+        scores(m);
+        mma_commit(&sfull[m]);
+      }
+      mma_commit(kempty);
+      for (int i = 0; i < nsteps && ok; ++i) {
+        ok = wait(vfull, n & 1);
+        for (int m = 0; m < tiles && ok; ++m) {
+          ok = wait(&pfull[m], done[m] & 1);
+          if (!ok) break;
+          tc_fence_after();
+          outputs(m, i == 0);
+          mma_commit(&opv[m]);
+          if (m == tiles - 1) mma_commit(vempty);
+          if (i + 1 < nsteps) {
+            // the next scores overwrite the weights this product reads
+            if (m == 0) ok = wait(kfull, (n + 1) & 1);
+            ok = ok && wait(&opv[m], done[m] & 1);
+            if (!ok) break;
+            tc_fence_after();
+            scores(m);
+            mma_commit(&sfull[m]);
+            if (m == tiles - 1) mma_commit(kempty);
+          }
+          ++done[m];
+        }
+        ++n;
+      }
+    }
+    // after a wait that gave up too, nothing may still write TMEM or read shared memory
+    // when the CTA leaves
+    int unused = 0;
+    mma_commit(drain);
+    mbar_wait_bounded(drain, 0, &unused, nullptr, kDrainNs);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 12) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <class C>
+size_t entries_of(int group, int batch, int64_t tokens) {
+  return static_cast<size_t>(tokens * group / C::ROWS + batch);
+}
+
+template <class C>
+size_t workspace_of(int group, int batch, int64_t tokens, int num_sms) {
+  const size_t e = entries_of<C>(group, batch, tokens);
+  return 16 + e * sizeof(KvEntry) + (e + 2) / 2 * 16 +
+         static_cast<size_t>(num_sms) * 2 * (sizeof(KvPart) + C::ROWS * 4 + static_cast<size_t>(C::ROWS) * C::D * 4);
+}
+
+template <class C>
+cudaError_t run_prefill(const KvAttnArgs &args, void *ws, int num_sms, unsigned long long timeout_ns, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_done{0};
+  cudaError_t e = smem_attr_once(reinterpret_cast<const void *>(k_kv_prefill<C>), C::SMEM_BYTES, attr_done);
+  if (e != cudaSuccess) return e;
+  if (num_sms > kMaxWorkers) num_sms = kMaxWorkers;
+  PrefillArgs p;
+  p.a = args;
+  p.timeout_ns = timeout_ns;
+  const size_t n = entries_of<C>(args.group, args.kb.batch, args.kb.tokens);
+  p.max_entries = static_cast<int>(n);
+  uint8_t *w = static_cast<uint8_t *>(ws);
+  p.count = reinterpret_cast<int *>(w);
+  w += 16;
+  p.entries = reinterpret_cast<KvEntry *>(w);
+  w += n * sizeof(KvEntry);
+  p.prefix = reinterpret_cast<int64_t *>(w);
+  w += (n + 2) / 2 * 16;
+  p.a.parts = reinterpret_cast<KvPart *>(w);
+  w += static_cast<size_t>(num_sms) * 2 * sizeof(KvPart);
+  p.a.part_lse = reinterpret_cast<float *>(w);
+  w += static_cast<size_t>(num_sms) * 2 * C::ROWS * 4;
+  p.a.part_o = reinterpret_cast<float *>(w);
+  if ((e = launch_k(k_kv_plan<C>, dim3(1), dim3(kPlanThreads), 0, st, 1, p)) != cudaSuccess) return e;
+  if ((e = launch_k(k_kv_prefill<C>, dim3(num_sms), dim3(C::THREADS), C::SMEM_BYTES, st, 1, p)) != cudaSuccess) return e;
+  constexpr int RPC = 8;
+  return launch_k(k_kv_join<C::D, C::ROWS, RPC>, dim3(num_sms - 1, C::ROWS / RPC), dim3(128), 0, st, 1, p.a);
+}
+
+}  // namespace
+
+size_t kv_prefill_workspace(int head_dim, int group, int batch, int64_t tokens, int num_sms) {
+  switch (head_dim) {
+    case 64: return workspace_of<PreCfg<64>>(group, batch, tokens, num_sms);
+    case 128: return workspace_of<PreCfg<128>>(group, batch, tokens, num_sms);
+    default: return workspace_of<PreCfg<256>>(group, batch, tokens, num_sms);
+  }
+}
+
+cudaError_t launch_kv_prefill(const KvAttnArgs &a, int head_dim, void *ws, int num_sms, unsigned long long timeout_ns,
+                              cudaStream_t st) {
+  switch (head_dim) {
+    case 64: return run_prefill<PreCfg<64>>(a, ws, num_sms, timeout_ns, st);
+    case 128: return run_prefill<PreCfg<128>>(a, ws, num_sms, timeout_ns, st);
+    default: return run_prefill<PreCfg<256>>(a, ws, num_sms, timeout_ns, st);
+  }
+}
+
+}  // namespace qlora

@@ -55,7 +55,10 @@ struct PreCfg {
   static constexpr int SP_COLS = D == 256 ? 192 : 128;
   static constexpr int O_COL = MT * SP_COLS;
   static constexpr int TMEM_COLS = 512;
-  static constexpr int THREADS = 13 * 32;
+  static constexpr int THREADS = 16 * 32;
+  // registers of a thread: softmax, decoding, the rest; together what the CTA starts with
+  static constexpr int REGS_SOFTMAX = 176, REGS_DECODE = 104, REGS_REST = 56;
+  static_assert(256 * REGS_SOFTMAX + 128 * REGS_DECODE + 128 * REGS_REST == 128 * THREADS, "register split");
   static constexpr int BARS = 15;
   static constexpr int MISC_FLOATS = 2 * N + 2 * NB * N + 2 * 4;
   static constexpr int MISC_BYTES = MISC_FLOATS * 4 + BARS * 8 + 32;
@@ -225,6 +228,14 @@ struct Line {
   }
 };
 
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&w)[4]) { ld_shared_v4(addr, w[0], w[1], w[2], w[3]); }
 
@@ -315,6 +326,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
   };
 
   if (warp < 8) {
+    regs_inc<C::REGS_SOFTMAX>();
     // ================================================================ softmax: one row per thread
     const int m = warp >> 2;
     const int r = tid & 127;
@@ -549,6 +561,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       }
     }
   } else if (warp < 12) {
+    regs_dec<C::REGS_DECODE>();
     // ================================================================ decoding: codes -> fp16 operands
     const int dw = warp - 8;
     constexpr int LPR = 32 / TW;                 // lanes per token
@@ -696,32 +709,37 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       __syncwarp();
       if (bad_page) kv_error(a.kb);
     }
-  } else if (lane == 0) {
+  } else {
+    regs_dec<C::REGS_REST>();
+    if (warp == 12 && lane == 0) {
     // ================================================================ MMA issue
     constexpr uint32_t idesc_s = idesc_f16(128, N, false), idesc_o = idesc_f16(128, 64, true);
     uint32_t n = 0;                 // steps of the CTA
     uint32_t done[2] = {0, 0};      // P V products of each row tile
     uint32_t queries[2] = {0, 0};
     bool ok = true;
+    // (descriptors are formed in the loops: kept in registers they would not fit)
     auto scores = [&](int m) {  // S_m = Q_m K^T
       const uint32_t d = tmem + m * C::SP_COLS;
+#pragma unroll 1
+      for (int blk = 0; blk < NB; ++blk) {
+        const uint64_t ad = smem_desc_sw128(q_smem + m * C::Q_BYTES + blk * 16384, 16, 1024);
+        const uint64_t bd = smem_desc_sw128(k_smem + blk * (N * 128), 16, 1024);
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const uint64_t ad = smem_desc_sw128(q_smem + m * C::Q_BYTES + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024);
-        const uint64_t bd = smem_desc_sw128(k_smem + (k >> 2) * (N * 128) + (k & 3) * 32, 16, 1024);
-        mma_bf16_ss(d, ad, bd, idesc_s, k > 0 ? 1u : 0u);
+        for (int k = 0; k < 4; ++k) mma_bf16_ss(d, ad + 2 * k, bd + 2 * k, idesc_s, blk + k > 0 ? 1u : 0u);
       }
     };
     auto outputs = [&](int m, bool first) {  // O_m,b += P_m,b V_b
       const uint32_t pt = tmem + m * C::SP_COLS + C::P_COL, d = tmem + C::O_COL + m * D;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
+#pragma unroll 1
+      for (int blk = 0; blk < NB; ++blk) {
+        const uint64_t bd = smem_desc_sw128(v_smem + blk * (N * 128), 8192, 1024);
 #pragma unroll
         for (int k = 0; k < N / 16; ++k) {
-          const uint32_t at = TW == 32 ? 32 * (k >> 1) + 16 * b + 8 * (k & 1) : 32 * k + 8 * b;
-          const uint64_t bd = smem_desc_sw128(v_smem + b * (N * 128) + k * 2048, 8192, 1024);
-          mma_bf16_ts(d + 64 * b, pt + at, bd, idesc_o, !first || k > 0 ? 1u : 0u);
+          const uint32_t at = TW == 32 ? 32 * (k >> 1) + 16 * blk + 8 * (k & 1) : 32 * k + 8 * blk;
+          mma_bf16_ts(d + 64 * blk, pt + at, bd + 128 * k, idesc_o, !first || k > 0 ? 1u : 0u);
         }
+      }
     };
     while (ok && line.next(sg)) {
       const int tiles = MT == 2 && sg.rows > 128 ? 2 : 1;
@@ -766,6 +784,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
     int unused = 0;
     mma_commit(drain);
     mbar_wait_bounded(drain, 0, &unused, nullptr, kDrainNs);
+    }
   }
   tc_fence_before();
   __syncthreads();

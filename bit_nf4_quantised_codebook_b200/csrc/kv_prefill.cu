@@ -22,7 +22,7 @@
 // Numbers: as in kv_attention.cu (levels and weights in fp16, everything else float32),
 // and one more rounding of level x constant to fp16 for the keys (2^-11).  Per row, weights
 // are 2^(s - r) * cV with one reference r for all blocks, renewed when some weight passes
-// 2^14 (then the largest contribution so far weighs 2^6 or more), so a block whose constants
+// about 2^14 (then the largest contribution so far weighs 2^6 or more), so a block whose constants
 // are below 2^-20 of another block's loses bits.  Constants are taken relative to the
 // largest exponent among 32 tokens, so no range of constants overflows float32.
 //
@@ -56,19 +56,30 @@ struct PreCfg {
   static constexpr int O_COL = MT * SP_COLS;
   static constexpr int TMEM_COLS = 512;
   static constexpr int THREADS = 16 * 32;
-  // registers of a thread: softmax, decoding, the rest; together what the CTA starts with
-  static constexpr int REGS_SOFTMAX = 176, REGS_DECODE = 104, REGS_REST = 56;
-  static_assert(256 * REGS_SOFTMAX + 128 * REGS_DECODE + 128 * REGS_REST == 128 * THREADS, "register split");
-  static constexpr int BARS = 15;
-  static constexpr int MISC_FLOATS = 2 * N + 2 * NB * N + 2 * 4;
-  static constexpr int MISC_BYTES = MISC_FLOATS * 4 + BARS * 8 + 32;
+  // registers of a thread: softmax and the others; together what the CTA starts with
+  static constexpr int REGS_SOFTMAX = 144, REGS_OTHERS = 112;
+  static_assert(256 * REGS_SOFTMAX + 256 * REGS_OTHERS == 128 * THREADS, "register split");
+  static constexpr int BARS = 19;
+  static constexpr int MISC_FLOATS = 2 * N + 2 * NB * N;
+  static constexpr int MISC_BYTES = MISC_FLOATS * 4 + 4 * 8 + 2 * 7 * 8 + BARS * 8 + 32;
   static constexpr int SMEM_BYTES = 0x20000 + KV_BYTES + MT * Q_BYTES;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
   static_assert(O_COL + MT * D <= TMEM_COLS, "TMEM columns");
 };
 
+// Binades between the largest and the smallest constant of a step up to which they are folded
+// into the fp16 operands: keys keep all their bits (fp16 has 25 binades below 2^12), and a
+// weight that vanishes in fp16 (2^-31 of the largest) can have a value 2^8 times another's.
+constexpr int kNearKeys = 12, kNearValues = 8;
 constexpr unsigned long long kDrainNs = 1000000000ull;  // bound on the wait for the MMAs in flight at the end
 
+// How a step's keys and values were written (by the decoding warps, for the others).  Where
+// the constants of a step lie close together they are folded into the fp16 operands; where
+// they do not (wide) they multiply the scores (cs) and the weights (cv), token by token.
+struct StepInfo {
+  float scale;  // keys: factor of the scores; values: the exponent that constants are relative to
+  int wide;
+};
 struct KvEntry {  // a row tile of a sequence; its heads follow one another on the line
   int b, tile;
   int lo;     // first cached token of its first step
@@ -185,49 +196,60 @@ struct Segment {
   int64_t first, end, at;  // the item's steps on the line, and where this part begins
 };
 
+// This worker's parts, in order.  A role keeps two integers between its parts, and reads
+// and computes the rest again when it needs it: state kept through the steps would be
+// spilled, and with all of shared memory in use a spilled value is a second-level cache
+// access away.
 template <class C>
-struct Line {
-  const PrefillArgs &p;
-  int64_t total, workers, me, begin, stop, at;
-  int e;
-  KvEntry t;
-  int64_t base, next_base;
-  __device__ __forceinline__ Line(const PrefillArgs &p_, int64_t total_, int e0)
-      : p(p_), total(total_), workers(gridDim.x), me(blockIdx.x), e(e0) {
-    begin = at = me * total / workers;
-    stop = (me + 1) * total / workers;
-    if (at < stop) load();
-  }
-  __device__ __forceinline__ void load() {
-    t = p.entries[e];
-    base = p.prefix[e];
-    next_base = p.prefix[e + 1];
-  }
-  __device__ __forceinline__ bool next(Segment &s) {
-    if (at >= stop) return false;
-    while (at >= next_base) {
-      ++e;
-      load();
-    }
-    const int64_t rel = at - base;
-    s.b = t.b;
-    s.tile = t.tile;
-    s.lo = t.lo;
-    s.head = static_cast<int>(rel / t.steps);
-    s.step0 = static_cast<int>(rel - static_cast<int64_t>(s.head) * t.steps);
-    s.first = base + static_cast<int64_t>(s.head) * t.steps;
-    s.end = s.first + t.steps;
-    s.step1 = stop < s.end ? static_cast<int>(stop - s.first) : t.steps;
-    s.whole = s.step0 == 0 && s.step1 == t.steps;
-    s.slot = at == begin ? 0 : 1;
-    s.at = at;
-    s.q = kv_seq(p.a.kb, s.b);
-    s.rows = min(s.q.n * p.a.group - s.tile * C::ROWS, C::ROWS);
-    at = s.first + s.step1;
-    return true;
-  }
-};
+__device__ __forceinline__ bool next_part(const PrefillArgs &p, int &e, int done, Segment &s) {
+  const int64_t total = p.prefix[*p.count], workers = gridDim.x, me = blockIdx.x;
+  const int64_t begin = me * total / workers, stop = (me + 1) * total / workers, at = begin + done;
+  if (at >= stop) return false;
+  while (at >= p.prefix[e + 1]) ++e;
+  const KvEntry t = p.entries[e];
+  const int64_t base = p.prefix[e], rel = at - base;
+  s.b = t.b;
+  s.tile = t.tile;
+  s.lo = t.lo;
+  s.head = static_cast<int>(rel / t.steps);
+  s.step0 = static_cast<int>(rel - static_cast<int64_t>(s.head) * t.steps);
+  s.first = base + static_cast<int64_t>(s.head) * t.steps;
+  s.end = s.first + t.steps;
+  s.step1 = stop < s.end ? static_cast<int>(stop - s.first) : t.steps;
+  s.whole = s.step0 == 0 && s.step1 == t.steps;
+  s.slot = at == begin ? 0 : 1;
+  s.at = at;
+  s.q = kv_seq(p.a.kb, s.b);
+  s.rows = min(s.q.n * p.a.group - s.tile * C::ROWS, C::ROWS);
+  return true;
+}
 
+// MMAs and commits by one elected lane of a converged warp (always the same one).
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(ad), "l"(bd), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t at, uint64_t bd, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(at), "l"(bd), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xFFFFFFFF;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -235,6 +257,30 @@ __device__ __forceinline__ void regs_inc() {
 template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// Two float32 in one 64-bit register, and the paired arithmetic of sm_100.
+__device__ __forceinline__ uint64_t pair_bits(uint32_t lo, uint32_t hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) { return pair_bits(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ float low(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x)); }
+__device__ __forceinline__ float high(uint64_t x) { return __uint_as_float(static_cast<uint32_t>(x >> 32)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&w)[4]) { ld_shared_v4(addr, w[0], w[1], w[2], w[3]); }
@@ -252,10 +298,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
   const uint32_t v_smem = table + 0x10000u, q_smem = v_smem + C::KV_BYTES;
   float *cs = reinterpret_cast<float *>(smem + (k_smem - smem_base) + C::KV_BYTES);  // [2][N] score factors
   float *cv = cs + 2 * N;                                                            // [2][NB][N] value constants
-  float *ec = cv + 2 * NB * N;                                                       // [2][4] their exponents
-  uint64_t *bars = reinterpret_cast<uint64_t *>(ec + 8);
+  StepInfo *kinfo = reinterpret_cast<StepInfo *>(cv + 2 * NB * N), *vinfo = kinfo + 2;  // [2] each
+  int2 *ranges = reinterpret_cast<int2 *>(vinfo + 2);                                // [2][7] of the decoding warps
+  uint64_t *bars = reinterpret_cast<uint64_t *>(ranges + 14);
   uint64_t *kfull = bars, *kempty = bars + 1, *vfull = bars + 2, *vempty = bars + 3, *cfull = bars + 4,
-           *sfull = bars + 6, *pfull = bars + 8, *opv = bars + 10, *qfull = bars + 12, *drain = bars + 14;
+           *sfull = bars + 6, *pfull = bars + 8, *opv = bars + 10, *qfull = bars + 12, *drain = bars + 14, *krange = bars + 15, *vrange = bars + 17;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::BARS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *s_entry = reinterpret_cast<int *>(tmem_slot + 2);
@@ -270,15 +317,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
   if (tid == 0) {
     mbar_init(kfull, 4);
     mbar_init(kempty, 1);
-    mbar_init(vfull, 4);
+    mbar_init(vfull, 3);
     mbar_init(vempty, 1);
     mbar_init(drain, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&cfull[i], 4);
+      mbar_init(&cfull[i], 7);
+      mbar_init(&krange[i], 4);
+      mbar_init(&vrange[i], 3);
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 128);
+      mbar_init(&pfull[i], 4);
       mbar_init(&opv[i], 1);
-      mbar_init(&qfull[i], 128);
+      mbar_init(&qfull[i], 4);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -294,10 +343,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
   }
   pdl_wait();
   pdl_launch_dependents();
-  const int count = *p.count;
-  const int64_t total = p.prefix[count];
   if (warp == 0) {  // the entry that holds this worker's first step: 32 probes at a time
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * total / gridDim.x;
+    const int count = *p.count;
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * p.prefix[count] / gridDim.x;
     int lo = 0, hi = count;
     while (hi - lo > 1) {
       const int stride = (hi - lo + 31) / 32;
@@ -318,9 +366,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  Line<C> line(p, total, *s_entry);
-  Segment sg;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  int entry = *s_entry, done_steps = 0;  // where this role is on the line
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     return mbar_wait_bounded(bar, parity, abort_flag, a.kb.dev_err, p.timeout_ns);
   };
@@ -335,10 +382,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
     uint32_t steps_done = 0;  // of this row tile
     uint32_t all_steps = 0;   // of the CTA
     bool ok = true;
-    while (ok && line.next(sg)) {
-      const int nsteps = sg.step1 - sg.step0;
+    while (ok) {
+      int nsteps, tok0, see_lo, see_hi;
+      float qs = 0.0f;
+      {
+      Segment sg;
+      if (!next_part<C>(p, entry, done_steps, sg)) break;
+      nsteps = sg.step1 - sg.step0;
       if (m * 128 >= sg.rows) {  // no row in this half
         all_steps += nsteps;
+        done_steps += nsteps;
         continue;
       }
       // ---- the query row: scaled to fp16, into the swizzled operand
@@ -346,7 +399,6 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       const bool live = row < sg.rows;
       const int rr = sg.tile * C::ROWS + row;
       const int tok = live ? rr / a.group : 0, h = live ? rr - tok * a.group : 0;
-      float qs = 0.0f;
       {
         const uint16_t *src = a.Q + static_cast<int64_t>(sg.q.row0 + tok) * a.q_token_stride +
                               static_cast<int64_t>(sg.head * a.group + h) * a.q_head_stride;
@@ -379,16 +431,18 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         qs = pow2(e) * a.scale_log2;
         if (mag >= 0x7F80u) qs = __uint_as_float(0x7FC00000u);  // a non-finite query: its row is NaN throughout
         fence_proxy_async_smem();
-        mbar_arrive(&qfull[m]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&qfull[m]);
       }
       const int pos = sg.q.pos0() + tok;
-      const int see_hi = !live ? 0x7FFFFFFF : a.causal ? min(sg.q.len, pos + 1) : sg.q.len;
-      const int see_lo = live && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      see_hi = !live ? 0x7FFFFFFF : a.causal ? min(sg.q.len, pos + 1) : sg.q.len;
+      see_lo = live && a.window > 0 ? max(0, pos - a.window + 1) : 0;
+      tok0 = sg.lo + sg.step0 * N;
+      }
 
       float ref = kFloor, mx = kFloor, rv = kFloor, l = 0.0f;
-      for (int step = sg.step0; step < sg.step1; ++step, ++steps_done, ++all_steps) {
+      for (int step = 0; step < nsteps; ++step, ++steps_done, ++all_steps, tok0 += N) {
         const int st = all_steps & 1;
-        const int tok0 = sg.lo + step * N;
         ok = wait(&cfull[st], (all_steps >> 1) & 1) && wait(&sfull[m], steps_done & 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
           ok = false;
@@ -396,114 +450,126 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         }
         tc_fence_after();
         const bool hide = __any_sync(0xFFFFFFFFu, tok0 < see_lo || tok0 + N > see_hi);
+        const StepInfo hk = kinfo[st], hv = vinfo[st];
+        const bool kwide = hk.wide != 0, vwide = hv.wide != 0;
+        const float e_c = hv.scale;
         const float *csr = cs + st * N, *cvr = cv + st * NB * N;
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        const float factor = hk.scale * qs;
+        // The usual pass over TW columns: v holds their products, w receives the weights; two
+        // columns per instruction where there is a paired one.
+        auto plain = [&](const uint32_t (&v)[TW], uint32_t (&w)[TW / 2], float &sum) -> bool {
+          const uint64_t f2 = pair(factor, factor), shift2 = pair(e_c - ref, e_c - ref);
+          uint64_t total0 = 0, total1 = 0;
+          __half2 most = __float2half2_rn(0.0f);
+#pragma unroll
+          for (int j = 0; j < TW; j += 4) {
+            const uint64_t x0 = fma2(pair_bits(v[j], v[j + 1]), f2, shift2);
+            const uint64_t x1 = fma2(pair_bits(v[j + 2], v[j + 3]), f2, shift2);
+            const float p0 = ex2(low(x0)), p1 = ex2(high(x0)), p2 = ex2(low(x1)), p3 = ex2(high(x1));
+            total0 = add2(total0, pair(p0, p1));
+            total1 = add2(total1, pair(p2, p3));
+            w[j / 2] = pack_half2(p0, p1);
+            w[j / 2 + 1] = pack_half2(p2, p3);
+            most = __hmax2(most, __hmax2(*reinterpret_cast<const __half2 *>(&w[j / 2]),
+                                         *reinterpret_cast<const __half2 *>(&w[j / 2 + 1])));
+          }
+          total0 = add2(total0, total1);
+          sum = low(total0) + high(total0);
+          return __low2float(most) > kMostWeight || __high2float(most) > kMostWeight;
+        };
+        // A pass where some row does not see every token, where constants multiply the weights, or
+        // where a weight passed its limit: the reference is renewed if one does, and what was
+        // accumulated and weighed so far follows.
+        auto careful = [&](int c, const uint32_t (&v)[TW], uint32_t (&w)[NB * TW / 2], float &sum) {
           float s[TW];
-          {
-            uint32_t v[TW];
-            if constexpr (TW == 32) tmem_ld32(s_tmem + c * TW, v);
-            else tmem_ld16(s_tmem + c * TW, v);
-            tmem_ld_wait();
+          float top = mx, big = rv;
 #pragma unroll
-            for (int j = 0; j < TW; j += 4) {
-              const float4 f = *reinterpret_cast<const float4 *>(csr + c * TW + j);
-              s[j] = __uint_as_float(v[j]) * f.x * qs;
-              s[j + 1] = __uint_as_float(v[j + 1]) * f.y * qs;
-              s[j + 2] = __uint_as_float(v[j + 2]) * f.z * qs;
-              s[j + 3] = __uint_as_float(v[j + 3]) * f.w * qs;
-            }
+          for (int j = 0; j < TW; ++j) {
+            const int t = tok0 + c * TW + j;
+            s[j] = __uint_as_float(v[j]) * (kwide ? csr[c * TW + j] : hk.scale) * qs;
+            if (t >= see_hi || t < see_lo) s[j] = -INFINITY;
           }
-          if (hide) {
+#pragma unroll 1
+          for (int pass = 0; pass < 2; ++pass) {
+            float most = 0.0f;
+            sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < TW; ++j) {
-              const int t = tok0 + c * TW + j;
-              if (t >= see_hi || t < see_lo) s[j] = -INFINITY;
-            }
-          }
-          const float e_c = ec[st * 4 + c];
-          uint32_t w[NB * TW / 2];
-          float sum;
-          auto weights = [&](bool hidden) -> bool {
-            const float off = ref - e_c;
-            float most = 0.0f, sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-            for (int j = 0; j < TW; j += 4) {
-              float pw[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) pw[i] = ex2(s[j + i] - off);
-              sum0 += pw[0] + pw[2];
-              sum1 += pw[1] + pw[3];
+            for (int j = 0; j < TW; j += 2) {
+              const float p0 = ex2(s[j] - (ref - e_c)), p1 = ex2(s[j + 1] - (ref - e_c));
+              sum += p0 + p1;
 #pragma unroll
               for (int k = 0; k < NB; ++k) {
-                const float4 f = *reinterpret_cast<const float4 *>(cvr + k * N + c * TW + j);
-                float x0 = pw[0] * f.x, x1 = pw[1] * f.y, x2 = pw[2] * f.z, x3 = pw[3] * f.w;
-                if (hidden) {  // a token that a row does not see adds nothing, whatever its value's constant
-                  x0 = s[j] == -INFINITY ? 0.0f : x0;
-                  x1 = s[j + 1] == -INFINITY ? 0.0f : x1;
-                  x2 = s[j + 2] == -INFINITY ? 0.0f : x2;
-                  x3 = s[j + 3] == -INFINITY ? 0.0f : x3;
-                }
-                most = fmaxf(most, fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)));
-                w[k * (TW / 2) + j / 2] = pack_half2(x0, x1);
-                w[k * (TW / 2) + j / 2 + 1] = pack_half2(x2, x3);
+                if (k > 0 && !vwide) continue;
+                const float c0 = vwide ? cvr[k * N + c * TW + j] : 1.0f, c1 = vwide ? cvr[k * N + c * TW + j + 1] : 1.0f;
+                // a token that a row does not see adds nothing, whatever its value's constant
+                const float w0 = s[j] == -INFINITY ? 0.0f : p0 * c0, w1 = s[j + 1] == -INFINITY ? 0.0f : p1 * c1;
+                most = fmaxf(most, fmaxf(w0, w1));
+                w[k * (TW / 2) + j / 2] = pack_half2(w0, w1);
               }
             }
-            sum = sum0 + sum1;
-            return most > kMostWeight || sum > kMostSum;
-          };
-          const bool over = hide ? weights(true) : weights(false);
-          if (__any_sync(0xFFFFFFFFu, over)) {
-            // renew the reference; what was accumulated and weighed so far follows
-            float top = mx;
+            if (pass == 1 || !__any_sync(0xFFFFFFFFu, most > kMostWeight || sum > kMostSum)) break;
 #pragma unroll
             for (int j = 0; j < TW; ++j) {
               top = fmaxf(top, s[j]);
+              if (!vwide) continue;
 #pragma unroll
-              for (int k = 0; k < NB; ++k) rv = fmaxf(rv, s[j] + lg2(cvr[k * N + c * TW + j]) + e_c);
+              for (int k = 0; k < NB; ++k) big = fmaxf(big, s[j] + lg2(cvr[k * N + c * TW + j]) + e_c);
             }
+            if (!vwide) big = fmaxf(big, top + e_c);
+            rv = big;
             const float next = ceilf(fmaxf(rv - kLift, top + e_c - 100.0f));
             const float f = next > ref ? ex2(ref - next) : 1.0f;  // a power of two
             ref = fmaxf(ref, next);
             l *= ex2(mx - top);
             mx = top;
             tmem_st_wait();
-            if (step > sg.step0) {
+            auto rescale = [&](uint32_t from, int cols, auto scale) {
 #pragma unroll 1
-              for (int k = 0; k < D; k += 32) {
-                uint32_t v[32];
-                tmem_ld32(o_tmem + k, v);
+              for (int k = 0; k < cols; k += 16) {
+                uint32_t o[16];
+                tmem_ld16(from + k, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * f);
-                tmem_st32(o_tmem + k, v);
+                for (int j = 0; j < 16; ++j) o[j] = scale(o[j]);
+                tmem_st16(from + k, o);
               }
-            }
+            };
+            if (step > 0)
+              rescale(o_tmem, D, [&](uint32_t x) { return __float_as_uint(__uint_as_float(x) * f); });
+            // the weights of the passes before this one (and whatever else those columns hold)
             const __half2 f2 = __float2half2_rn(f);
-#pragma unroll 1
-            for (int k = 0; k < c; ++k) {
-              uint32_t v[NB * TW / 2];
-              if constexpr (NB == 1) tmem_ld16(p_tmem + k * 32, v);
-              else tmem_ld32(p_tmem + k * 32, v);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < NB * TW / 2; ++j) {
-                const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&v[j]), f2);
-                v[j] = *reinterpret_cast<const uint32_t *>(&x);
-              }
-              if constexpr (NB == 1) tmem_st16(p_tmem + k * 32, v);
-              else tmem_st32(p_tmem + k * 32, v);
-            }
+            rescale(p_tmem, c * 32, [&](uint32_t x) {
+              const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&x), f2);
+              return *reinterpret_cast<const uint32_t *>(&y);
+            });
             tmem_st_wait();
-            weights(true);
+          }
+        };
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t v[TW], w[NB * TW / 2];
+          float sum;
+          if constexpr (TW == 32) tmem_ld32(s_tmem + c * TW, v);
+          else tmem_ld16(s_tmem + c * TW, v);
+          tmem_ld_wait();
+          if (hide || kwide || vwide ||
+              __any_sync(0xFFFFFFFFu, plain(v, reinterpret_cast<uint32_t(&)[TW / 2]>(w), sum))) {
+            careful(c, v, w, sum);
           }
           l = fmaf(sum, ex2(ref - e_c - mx), l);
-          if constexpr (NB == 1) tmem_st16(p_tmem + c * 32, w);
-          else tmem_st32(p_tmem + c * 32, w);
+          const uint32_t to = p_tmem + c * 32;  // over the scores just read, or apart from them
+          if (!vwide) {
+            if constexpr (TW == 32) tmem_st16(to, reinterpret_cast<const uint32_t(&)[16]>(w));
+            else tmem_st8(to, reinterpret_cast<const uint32_t(&)[8]>(w));
+          } else {
+            if constexpr (NB == 1) tmem_st16(to, w);
+            else tmem_st32(to, w);
+          }
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&pfull[m]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[m]);
       }
       if (!ok) break;
       // ---- the outputs of this part of the item
@@ -513,6 +579,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         break;
       }
       tc_fence_after();
+      Segment sg;
+      next_part<C>(p, entry, done_steps, sg);
+      done_steps += nsteps;
+      const int row = m * 128 + r, rr = sg.tile * C::ROWS + row;
+      const bool live = row < sg.rows;
+      const int tok = live ? rr / a.group : 0, h = live ? rr - tok * a.group : 0;
       const bool any = l > 0.0f || l != l;
       const float half_unit = ex2(0.5f * (ref - mx));  // applied twice: it may pass float32's exponents
       const float inv = any ? a.v_unit / l * half_unit : 0.0f;
@@ -545,8 +617,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       if (!sg.whole) {
         if (live) a.part_lse[part * C::ROWS + row] = any ? mx + lg2(l) : -INFINITY;
         if (tid == 0) {
+          const int64_t total = p.prefix[*p.count];
+          const int64_t workers = gridDim.x;
           // the worker that holds step u is the largest g with g * total / workers <= u
-          auto worker_of = [&](int64_t u) { return static_cast<int>(((u + 1) * line.workers - 1) / total); };
+          auto worker_of = [&](int64_t u) { return static_cast<int>(((u + 1) * workers - 1) / total); };
           KvPart kp;
           kp.present = 1;
           kp.b = sg.b;
@@ -554,225 +628,304 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           kp.tile = sg.tile;
           kp.g0 = worker_of(sg.first);
           kp.last = worker_of(sg.end - 1);
-          kp.head_slot = kp.g0 * total / line.workers == sg.first ? 0 : 1;
-          kp.joins = sg.at != sg.first && sg.at == (kp.g0 + 1) * total / line.workers ? 1 : 0;
+          kp.head_slot = kp.g0 * total / workers == sg.first ? 0 : 1;
+          kp.joins = sg.at != sg.first && sg.at == (kp.g0 + 1) * total / workers ? 1 : 0;
           a.parts[part] = kp;
         }
       }
     }
-  } else if (warp < 12) {
-    regs_dec<C::REGS_DECODE>();
+  } else {
+    regs_dec<C::REGS_OTHERS>();
+    if (warp != 12) {
     // ================================================================ decoding: codes -> fp16 operands
-    const int dw = warp - 8;
-    constexpr int LPR = 32 / TW;                 // lanes per token
-    constexpr int PASSES = D / 32 / LPR;         // 16-byte pieces of codes per lane and side
-    const int sub = LPR == 2 ? lane & 1 : 0;
-    const int tr = dw * TW + lane / LPR;         // token of the step
+    // Four warps for the keys, three for the values.  A unit is a tile of 16 tokens (inside one
+    // page): two lanes per token.
+    const bool keys = warp < 12;
+    const int dw = keys ? warp - 8 : warp - 13, warps = keys ? 4 : 3;
+    constexpr int TILES = N / 16, MINE = (TILES + 2) / 3;  // tiles dw, dw + warps, ...: at most MINE
+    constexpr int PASSES = D / 64;                         // 16-byte pieces of codes per lane and tile
+    const int sub = lane & 1, tok = lane >> 1;
     const uint32_t tab = table | (lane * 4);
-    // raw codes of this warp's tokens, in the table's gaps: 128 bytes of every 256
-    auto gap = [&](int stage, int side, int off) {
-      return table + 128u + static_cast<uint32_t>(stage) * 32768u + static_cast<uint32_t>(side) * 16384u +
+    const uint8_t *codes = keys ? a.k_codes : a.v_codes;
+    const uint16_t *absmax = keys ? a.k_absmax : a.v_absmax;
+    uint64_t *full = keys ? kfull : vfull, *empty = keys ? kempty : vempty, *range = keys ? krange : vrange;
+    const uint32_t operand = keys ? k_smem : v_smem;
+    int2 *my_ranges = ranges + (keys ? 0 : 4);
+    const int near = keys ? kNearKeys : kNearValues;
+    // raw codes, in the table's gaps: 128 bytes of every 256
+    auto gap = [&](int stage, int off) {
+      return table + 128u + static_cast<uint32_t>(stage) * 32768u + (keys ? 0u : 16384u) +
              static_cast<uint32_t>((off >> 7) * 256 + (off & 127));
     };
     uint32_t n = 0;  // steps of the CTA so far
     bool ok = true;
-    while (ok && line.next(sg)) {
-      const int32_t *pages = a.kb.page_table + static_cast<int64_t>(sg.b) * a.kb.max_pages;
+    while (ok) {
+      int lo, nsteps, head, len;
+      const int32_t *pages;
+      {
+        Segment sg;
+        if (!next_part<C>(p, entry, done_steps, sg)) break;
+        nsteps = sg.step1 - sg.step0;
+        lo = sg.lo + sg.step0 * N;
+        head = sg.head;
+        len = sg.q.len;
+        pages = a.kb.page_table + static_cast<int64_t>(sg.b) * a.kb.max_pages;
+        done_steps += nsteps;
+      }
       bool bad_page = false;
-      constexpr int TILES = TW / 16;  // a warp's tokens in tiles of 16, each inside one page
-      auto load_pages = [&](int step, int (&page)[TILES]) {
+      auto tile_of = [&](int i) { return dw + i * warps; };
+      auto load_pages = [&](int step, int (&page)[MINE]) {
 #pragma unroll
-        for (int i = 0; i < TILES; ++i)
-          page[i] = __ldg(pages + min((sg.lo + step * N + dw * TW + 16 * i) >> a.kb.page_shift, a.kb.max_pages - 1));
+        for (int i = 0; i < MINE; ++i)
+          page[i] = __ldg(pages + min((lo + step * N + 16 * tile_of(i)) >> a.kb.page_shift, a.kb.max_pages - 1));
       };
-      uint32_t kcon[NB], vcon[NB];  // constants of this lane's token, as loaded for the step to come
-      auto fetch = [&](int step, const int (&page)[TILES], int stage) {
-        uint32_t row[TILES];
+      uint32_t con[MINE][(NB + 1) / 2];  // constants of this lane's tokens, as loaded for the step to come
+      auto fetch = [&](int step, const int (&page)[MINE], int stage) {
 #pragma unroll
-        for (int i = 0; i < TILES; ++i) {
-          const int t = sg.lo + step * N + dw * TW + 16 * i;
+        for (int i = 0; i < MINE; ++i) {
+          if (tile_of(i) >= TILES) continue;
+          const int t = lo + step * N + 16 * tile_of(i);
           const bool bad = static_cast<unsigned>(page[i]) >= static_cast<unsigned>(a.kb.num_pages);
-          bad_page |= bad && t < sg.q.len;
-          row[i] = bad ? 0
-                       : ((static_cast<uint32_t>(page[i]) * a.heads + sg.head) << a.kb.page_shift) +
-                             (t & ((1 << a.kb.page_shift) - 1));
+          bad_page |= bad && t < len;
+          const uint32_t row = bad ? 0
+                                   : ((static_cast<uint32_t>(page[i]) * a.heads + head) << a.kb.page_shift) +
+                                         (t & ((1 << a.kb.page_shift) - 1));
+          const uint8_t *src = codes + static_cast<uint64_t>(row) * (D / 2) + lane * 16;
 #pragma unroll
-          for (int x = 0; x < (8 * D + 511) / 512; ++x) {  // 8 D bytes of codes per tile and side
-            const int off = (dw * TW + 16 * i) * (D / 2) + x * 512 + lane * 16;
-            copy16(gap(stage, 0, off), a.k_codes + static_cast<uint64_t>(row[i]) * (D / 2) + x * 512 + lane * 16);
-            copy16(gap(stage, 1, off), a.v_codes + static_cast<uint64_t>(row[i]) * (D / 2) + x * 512 + lane * 16);
+          for (int x = 0; x < D / 64; ++x)  // 8 D bytes of codes per tile
+            copy16(gap(stage, tile_of(i) * 8 * D + x * 512 + lane * 16), src + x * 512);
+          const uint16_t *pc = absmax + (static_cast<uint64_t>(row) + tok) * NB;
+          if constexpr (NB == 1) con[i][0] = __ldg(pc);
+          if constexpr (NB == 2) con[i][0] = __ldg(reinterpret_cast<const uint32_t *>(pc));
+          if constexpr (NB == 4) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(pc));
+            con[i][0] = u.x;
+            con[i][(NB + 1) / 2 - 1] = u.y;
           }
         }
         copies_commit();
-        const int in_warp = lane / LPR;
-        const uint64_t crow = static_cast<uint64_t>(row[TILES == 2 ? in_warp >> 4 : 0]) + (in_warp & 15);
-#pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          kcon[k] = __ldg(a.k_absmax + crow * NB + k);
-          vcon[k] = __ldg(a.v_absmax + crow * NB + k);
-        }
       };
-      int page[TILES];
-      load_pages(sg.step0, page);
-      fetch(sg.step0, page, n & 1);
-      load_pages(sg.step0 + 1, page);
-      for (int step = sg.step0; step < sg.step1; ++step, ++n) {
+      int page[MINE];
+      load_pages(0, page);
+      fetch(0, page, n & 1);
+      load_pages(1, page);
+      for (int step = 0; step < nsteps; ++step, ++n) {
         const int st = n & 1;
-        uint32_t kb[NB], vb[NB];
+        // ---- the range of the step's constants
+        uint32_t bits[MINE][NB];
+        uint32_t most = 0, least = 0xFFFFu;
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          kb[k] = kcon[k];
-          vb[k] = vcon[k];
-        }
-        if (step + 1 < sg.step1) {
+        for (int i = 0; i < MINE; ++i)
+#pragma unroll
+          for (int k = 0; k < NB; ++k) {
+            const uint32_t c = k & 1 ? con[i][k / 2] >> 16 : con[i][k / 2] & 0xFFFFu;
+            // no tile, or behind the sequence: anything, and masked
+            const bool none = tile_of(i) >= TILES || lo + step * N + 16 * tile_of(i) + tok >= len;
+            bits[i][k] = none ? 0 : c;
+            most = max(most, bits[i][k]);
+            if (bits[i][k] != 0) least = min(least, bits[i][k]);
+          }
+        if (step + 1 < nsteps) {
           fetch(step + 1, page, st ^ 1);
           load_pages(step + 2, page);
           copies_wait<1>();
         } else {
           copies_wait<0>();
         }
-        __syncwarp();
-        if (n > 0) ok = wait(kempty, (n - 1) & 1);
+        most = __reduce_max_sync(0xFFFFFFFFu, most);
+        least = __reduce_min_sync(0xFFFFFFFFu, least);
+        if (lane == 0) {
+          my_ranges[st * 7 + dw] = make_int2(most, least);
+          mbar_arrive(&range[st]);
+        }
+        ok = wait(&range[st], (n >> 1) & 1);
+        // (the factors of the scores are rewritten: no one may still read those of two steps ago)
+        if (ok && keys && n > 0) ok = wait(empty, (n - 1) & 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
           ok = false;
           break;
         }
-        // ---- constants: keys as fp16 below 2^12 and a power of two per token, values relative
-        // to the warp's largest exponent
-        uint32_t kmax = 0, vmax = 0;
-#pragma unroll
-        for (int k = 0; k < NB; ++k) {
-          kmax = max(kmax, kb[k]);
-          vmax = max(vmax, vb[k] < 0x7F80u ? vb[k] : 0u);
+        for (int i = 0; i < warps; ++i) {
+          const int2 o = my_ranges[st * 7 + i];
+          most = max(most, static_cast<uint32_t>(o.x));
+          least = min(least, static_cast<uint32_t>(o.y));
         }
-        const int ke = max(static_cast<int>(kmax >> 7) - 127, -110);
-        const bool kbad = kmax >= 0x7F80u;
-        const float kdown = kbad ? 0.0f : pow2(11 - ke);
-        __half2 kc[NB];
+        // ---- constants: folded into the operands (keys below 2^12, values below 2), or apart
+        auto exponent = [](uint32_t b) { return static_cast<int>(b >> 7) - 127; };
+        const int e = most ? exponent(most) : 0;
+        const bool wide = most >= 0x7F80u || e < -100 || e > 110 || (most && e - exponent(least) > near);
+        __half2 hc[MINE][NB];
+        if (!wide) {
+          const float f = pow2(keys ? 11 - e : -e);
 #pragma unroll
-        for (int k = 0; k < NB; ++k)
-          kc[k] = kbad ? __float2half2_rn(0.0f) : __float2half2_rn(__uint_as_float(kb[k] << 16) * kdown);
-        vmax = __reduce_max_sync(0xFFFFFFFFu, vmax);
-        const int ve = min(max(static_cast<int>(vmax >> 7) - 127, -100), 126);
-        if (sub == 0) {
-          cs[st * N + tr] = kbad ? __uint_as_float(0x7FC00000u) : pow2(ke - 11);
+          for (int i = 0; i < MINE; ++i)
 #pragma unroll
-          for (int k = 0; k < NB; ++k)
-            cv[(st * NB + k) * N + tr] =
-                vb[k] >= 0x7F80u ? __uint_as_float(0x7FC00000u) : __uint_as_float(vb[k] << 16) * pow2(-ve);
+            for (int k = 0; k < NB; ++k) hc[i][k] = __float2half2_rn(__uint_as_float(bits[i][k] << 16) * f);
+          if (dw == 0 && lane == 0) {
+            if (keys) kinfo[st] = StepInfo{pow2(e - 11), 0};
+            else vinfo[st] = StepInfo{static_cast<float>(e), 0};
+          }
+        } else if (keys) {
+          // each token's keys relative to their own exponent
+#pragma unroll
+          for (int i = 0; i < MINE; ++i) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < NB; ++k) top = max(top, bits[i][k]);
+            const int te = max(exponent(top), -110);
+            const bool bad = top >= 0x7F80u;
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+              hc[i][k] = __float2half2_rn(bad ? 0.0f : __uint_as_float(bits[i][k] << 16) * pow2(11 - te));
+            if (sub == 0 && tile_of(i) < TILES)
+              cs[st * N + 16 * tile_of(i) + tok] = bad ? __uint_as_float(0x7FC00000u) : pow2(te - 11);
+          }
+          if (dw == 0 && lane == 0) kinfo[st] = StepInfo{1.0f, 1};
+        } else {
+          // levels alone; the constants, as float32, multiply the weights
+          const int top = most >= 0x7F80u ? 0 : e;
+          const int base = top > 80 ? top - 80 : top < -100 ? max(top, -126) : 0;
+#pragma unroll
+          for (int i = 0; i < MINE; ++i)
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+              hc[i][k] = __float2half2_rn(1.0f);
+              if (sub == 0 && tile_of(i) < TILES)
+                cv[(st * NB + k) * N + 16 * tile_of(i) + tok] = bits[i][k] >= 0x7F80u
+                                                                    ? __uint_as_float(0x7FC00000u)
+                                                                    : __uint_as_float(bits[i][k] << 16) * pow2(-base);
+            }
+          if (dw == 0 && lane == 0) vinfo[st] = StepInfo{static_cast<float>(base), 1};
         }
-        if (lane == 0) ec[st * 4 + dw] = static_cast<float>(ve);
         __syncwarp();
         if (lane == 0) mbar_arrive(&cfull[st]);
-        // ---- codes of this lane's token: 16 bytes (32 channels) at a time, in an order that
-        // keeps eight neighbouring lanes out of each other's banks
-        auto decode = [&](int side, uint32_t dst, auto scale) {
+        if (!keys && n > 0) ok = wait(empty, (n - 1) & 1);
+        if (!__all_sync(0xFFFFFFFFu, ok)) {
+          ok = false;
+          break;
+        }
+        // ---- codes: 16 bytes (32 channels) of a token at a time, in an order of pieces and words
+        // that keeps eight neighbouring lanes (4 tokens) out of each other's banks
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+          if (tile_of(i) >= TILES) continue;
+          const int tr = 16 * tile_of(i) + tok;
 #pragma unroll
           for (int it = 0; it < PASSES; ++it) {
-            const int q = NB == 1 ? it ^ ((tr >> 2) & 1) : NB == 2 ? it ^ ((tr >> 1) & 3) : 4 * sub + (it ^ (tr & 3));
+            const int q = NB == 1 ? sub : NB == 2 ? 2 * sub + (it ^ ((tr >> 1) & 1)) : 4 * sub + (it ^ (tr & 3));
             uint32_t w[4];
-            lds128(gap(st, side, tr * (D / 2) + q * 16), w);
-            const uint32_t out = dst + (q >> 1) * (N * 128) + tr * 128;
+            lds128(gap(st, tr * (D / 2) + q * 16), w);
+            constexpr int SWAP = NB == 1 ? 0 : NB == 2 ? 2 : 1;
+            const int swap = sub * SWAP;
+            if constexpr (SWAP != 0) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (j < (j ^ SWAP)) {
+                  const uint32_t x = w[j], y = w[j ^ SWAP];
+                  w[j] = sub ? y : x;
+                  w[j ^ SWAP] = sub ? x : y;
+                }
+            }
+            __half2 f = hc[i][0];
+#pragma unroll
+            for (int k = 1; k < NB; ++k)
+              if ((q >> 1) == k) f = hc[i][k];
+            const uint32_t out = operand + (q >> 1) * (N * 128) + tr * 128;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t o[4] = {lookup<0>(w[j], tab), lookup<1>(w[j], tab), lookup<2>(w[j], tab), lookup<3>(w[j], tab)};
-              scale(o, q >> 1);
-              st_shared_v4(out + ((((q & 1) * 4 + j) ^ (tr & 7)) << 4), o[0], o[1], o[2], o[3]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&o[x]), f);
+                o[x] = *reinterpret_cast<const uint32_t *>(&y);
+              }
+              st_shared_v4(out + ((((q & 1) * 4 + (j ^ swap)) ^ (tr & 7)) << 4), o[0], o[1], o[2], o[3]);
             }
           }
-        };
-        decode(0, k_smem, [&](uint32_t (&o)[4], int blk) {
-          __half2 c = kc[0];
-#pragma unroll
-          for (int k = 1; k < NB; ++k)
-            if (blk == k) c = kc[k];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&o[i]), c);
-            o[i] = *reinterpret_cast<const uint32_t *>(&x);
-          }
-        });
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(kfull);
-        if (n > 0) ok = wait(vempty, (n - 1) & 1);
-        if (!__all_sync(0xFFFFFFFFu, ok)) {
-          ok = false;
-          break;
         }
-        decode(1, v_smem, [](uint32_t (&)[4], int) {});
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(vfull);
+        if (lane == 0) mbar_arrive(full);
       }
       copies_wait<0>();
       __syncwarp();
       if (bad_page) kv_error(a.kb);
     }
-  } else {
-    regs_dec<C::REGS_REST>();
-    if (warp == 12 && lane == 0) {
+    } else {
+    // all lanes run the loop, so that addresses stay in uniform registers; one issues
     // ================================================================ MMA issue
-    constexpr uint32_t idesc_s = idesc_f16(128, N, false), idesc_o = idesc_f16(128, 64, true);
+    constexpr uint32_t idesc_s = idesc_f16(128, N, false), idesc_o = idesc_f16(128, D, true),
+                       idesc_ob = idesc_f16(128, 64, true);
     uint32_t n = 0;                 // steps of the CTA
     uint32_t done[2] = {0, 0};      // P V products of each row tile
     uint32_t queries[2] = {0, 0};
     bool ok = true;
-    // (descriptors are formed in the loops: kept in registers they would not fit)
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+    const uint64_t q_desc = smem_desc_sw128(q_smem, 16, 1024), k_desc = smem_desc_sw128(k_smem, 16, 1024),
+                   v_desc = smem_desc_sw128(v_smem, N * 128, 1024);
     auto scores = [&](int m) {  // S_m = Q_m K^T
-      const uint32_t d = tmem + m * C::SP_COLS;
-#pragma unroll 1
-      for (int blk = 0; blk < NB; ++blk) {
-        const uint64_t ad = smem_desc_sw128(q_smem + m * C::Q_BYTES + blk * 16384, 16, 1024);
-        const uint64_t bd = smem_desc_sw128(k_smem + blk * (N * 128), 16, 1024);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mma_bf16_ss(d, ad + 2 * k, bd + 2 * k, idesc_s, blk + k > 0 ? 1u : 0u);
+      for (int k = 0; k < D / 16; ++k)
+        mma_f16_ss(tmem + m * C::SP_COLS, q_desc + ((m * C::Q_BYTES + (k >> 2) * 16384 + (k & 3) * 32) >> 4),
+                   k_desc + (((k >> 2) * (N * 128) + (k & 3) * 32) >> 4), idesc_s, k > 0 ? 1u : 0u);
+    };
+    auto outputs = [&](int m, bool first, bool wide) {  // O_m += P_m V, or O_m,b += P_m,b V_b block by block
+      const uint32_t d = tmem + C::O_COL + m * D, pt = tmem + m * C::SP_COLS + C::P_COL;
+      if (!wide) {
+#pragma unroll
+        for (int k = 0; k < N / 16; ++k)
+          mma_f16_ts(d, pt + (TW == 32 ? 32 * (k >> 1) + 8 * (k & 1) : 32 * k), v_desc + (k * 2048 >> 4), idesc_o,
+                     !first || k > 0 ? 1u : 0u);
+      } else {
+#pragma unroll 1
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int k = 0; k < N / 16; ++k) {
+            const int at = TW == 32 ? 32 * (k >> 1) + 16 * b + 8 * (k & 1) : 32 * k + 8 * b;
+            mma_f16_ts(d + 64 * b, pt + at, v_desc + ((b * (N * 128) + k * 2048) >> 4), idesc_ob,
+                       !first || k > 0 ? 1u : 0u);
+          }
       }
     };
-    auto outputs = [&](int m, bool first) {  // O_m,b += P_m,b V_b
-      const uint32_t pt = tmem + m * C::SP_COLS + C::P_COL, d = tmem + C::O_COL + m * D;
-#pragma unroll 1
-      for (int blk = 0; blk < NB; ++blk) {
-        const uint64_t bd = smem_desc_sw128(v_smem + blk * (N * 128), 8192, 1024);
-#pragma unroll
-        for (int k = 0; k < N / 16; ++k) {
-          const uint32_t at = TW == 32 ? 32 * (k >> 1) + 16 * blk + 8 * (k & 1) : 32 * k + 8 * blk;
-          mma_bf16_ts(d + 64 * blk, pt + at, bd + 128 * k, idesc_o, !first || k > 0 ? 1u : 0u);
-        }
+    while (ok) {
+      int tiles, nsteps;
+      {
+        Segment sg;
+        if (!next_part<C>(p, entry, done_steps, sg)) break;
+        tiles = MT == 2 && sg.rows > 128 ? 2 : 1;
+        nsteps = sg.step1 - sg.step0;
+        done_steps += nsteps;
       }
-    };
-    while (ok && line.next(sg)) {
-      const int tiles = MT == 2 && sg.rows > 128 ? 2 : 1;
-      const int nsteps = sg.step1 - sg.step0;
-      for (int m = 0; m < tiles && ok; ++m) ok = wait(&qfull[m], queries[m]++ & 1);
-      if (ok) ok = wait(kfull, n & 1);
+      for (int m = 0; m < tiles && ok; ++m) ok = wait_all(&qfull[m], queries[m]++ & 1);
+      if (ok) ok = wait_all(kfull, n & 1);
       if (!ok) break;
       tc_fence_after();
       // the previous item's outputs have been waited for by its softmax warps, which then
       // announced these queries
       for (int m = 0; m < tiles; ++m) {
         scores(m);
-        mma_commit(&sfull[m]);
+        commit(&sfull[m]);
       }
-      mma_commit(kempty);
+      commit(kempty);
       for (int i = 0; i < nsteps && ok; ++i) {
-        ok = wait(vfull, n & 1);
+        ok = wait_all(vfull, n & 1);
+        const bool wide = __shfl_sync(0xFFFFFFFFu, vinfo[n & 1].wide, 0) != 0;
         for (int m = 0; m < tiles && ok; ++m) {
-          ok = wait(&pfull[m], done[m] & 1);
+          ok = wait_all(&pfull[m], done[m] & 1);
           if (!ok) break;
           tc_fence_after();
-          outputs(m, i == 0);
-          mma_commit(&opv[m]);
-          if (m == tiles - 1) mma_commit(vempty);
+          outputs(m, i == 0, wide);
+          commit(&opv[m]);
+          if (m == tiles - 1) commit(vempty);
           if (i + 1 < nsteps) {
             // the next scores overwrite the weights this product reads
-            if (m == 0) ok = wait(kfull, (n + 1) & 1);
-            ok = ok && wait(&opv[m], done[m] & 1);
+            if (m == 0) ok = wait_all(kfull, (n + 1) & 1);
+            ok = ok && wait_all(&opv[m], done[m] & 1);
             if (!ok) break;
             tc_fence_after();
             scores(m);
-            mma_commit(&sfull[m]);
-            if (m == tiles - 1) mma_commit(kempty);
+            commit(&sfull[m]);
+            if (m == tiles - 1) commit(kempty);
           }
           ++done[m];
         }
@@ -782,7 +935,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
     // after a wait that gave up too, nothing may still write TMEM or read shared memory
     // when the CTA leaves
     int unused = 0;
-    mma_commit(drain);
+    commit(drain);
     mbar_wait_bounded(drain, 0, &unused, nullptr, kDrainNs);
     }
   }

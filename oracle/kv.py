@@ -48,13 +48,18 @@ def attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, causal:
     """One sequence.  q [n, Hq, D], k and v [len, H, D], all float64; the rows are
     the last n positions.  Returns (out [n, Hq, D], bound [n, Hq, D]).
 
-    The bound: a score is off by at most ds = S * (2^-11 + 2^-14) with S = scale *
-    sum |q_d k_d| (levels rounded to fp16, half a step 2^-11, for NF4 alone; float32
-    sums of D products, exponents and logarithms: 2^-14), so a softmax weight by a
-    factor within exp(+-2 ds); weights and values' levels are rounded to fp16 (2^-11
-    each, the levels for NF4 alone); weights below 2^-25 of the step of the largest
-    contribution vanish (2^-31 of it for each token); float32 sums and the joins of
-    parts add 2^-14; the output is rounded to bfloat16 (2^-8)."""
+    The bound: a score is off by at most ds = S * (2^-10 + 2^-14) with S = scale *
+    sum |q_d k_d|: for NF4 alone the levels are rounded to fp16 (half a step, 2^-11)
+    and, where many rows share the decoded keys, level * constant once more (2^-11;
+    the other code books' levels are multiples of at most 3 bits, exact in both);
+    float32 sums of D products, exponents and logarithms: 2^-14.  So a softmax weight
+    is off by a factor within exp(+-2 ds).  Weights are rounded to fp16 (2^-11), and
+    for NF4 alone the values' levels (2^-11) and, where many rows share them, level *
+    constant (2^-11); a token's weight that is 2^-31 of the largest vanishes, and its
+    value may be 2^8 times the largest one's (2^-23 for each token); float32 sums and
+    the joins of parts add 2^-14; the output is rounded to bfloat16 (2^-8, and half
+    the smallest subnormal).
+    """
     n, hq, d = q.shape
     length, h, _ = k.shape
     g = hq // h
@@ -80,13 +85,18 @@ def attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, causal:
         total = p.sum(1)
         p = p / np.where(total > 0, total, 1.0)[:, None]
         out[:, x] = p @ vv
-        ds = np.where(see, mag, 0.0).max(1) * ((2.0 ** -11 if nf4_levels else 0.0) + 2.0 ** -14)
-        rel = np.expm1(2 * ds) + 2.0 ** -11 * (2 if nf4_levels else 1) + 2.0 ** -14
+        ds = np.where(see, mag, 0.0).max(1) * ((2.0 ** -10 if nf4_levels else 0.0) + 2.0 ** -14)
+        with np.errstate(over="ignore"):
+            rel = np.expm1(2 * ds) + 2.0 ** -11 * (3 if nf4_levels else 1) + 2.0 ** -14
         spread = p @ np.abs(vv)
         # contributions to a block of 64 channels: weight times the block's largest magnitude
         big = np.abs(vv).reshape(length, -1, BLOCK).max(2)
         most = (p[:, :, None] * big[None]).max(1)
-        lost = np.repeat(most, BLOCK, axis=1) * length * 2.0 ** -31
-        bound[:, x] = rel[:, None] * spread + lost
+        lost = np.repeat(most, BLOCK, axis=1) * length * 2.0 ** -23
+        # two averages of the visible values are never further apart than twice the largest
+        span = 2 * np.where(see[:, :, None], np.abs(vv)[None], 0.0).max(1)
+        with np.errstate(over="ignore", invalid="ignore"):
+            moved = rel[:, None] * spread
+        bound[:, x] = np.minimum(np.where(np.isnan(moved), np.inf, moved), span) + lost
         bound[:, x] += 2.0 ** -8 * (np.abs(out[:, x]) + bound[:, x]) + 2.0 ** -133
     return out, bound

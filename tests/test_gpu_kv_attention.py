@@ -90,67 +90,95 @@ def test_scales(scale, q_scale):
     _run(Case([1, 2], [100, 400], page_size=32, seed=7), 2, 4, 128, scale=scale, q_scale=q_scale)
 
 
-def _values_of_any_size(dim, hidden):
-    """Constants of the values from 2^-100 to 2^100, those of hidden or unlikely tokens the largest."""
+def _constants_of_any_size(dim, n, side, exps):
+    """The constants of token j's keys or values times 2^exps[j]."""
     a = api()
     rng = np.random.default_rng(50)
-    case = Case([2], [90], page_size=16, seed=8)
+    case = Case([n], [90], page_size=16, seed=8)
     c, mirror = filled_cache(a, case, 1, dim, "nf4", rng)
-    exps = rng.integers(-100, 0, 90)
-    exps[[3, 88]] = -100
-    if hidden:
-        exps[89] = 100  # hidden from the first row, seen by the second
-    k, v = mirror[0]
-    v = v * 2.0 ** exps[:, None, None]
     p = np.arange(90)
     page, slot = case.table[0, p // 16], p % 16
-    _, absmax = kv.encode(bits(bf16(v)), "nf4")
-    full = bits(c.v_absmax).copy()
-    old = nf4.bf16_to_f64(full[page, :, slot])
-    full[page, :, slot] = bits(bf16(old * 2.0 ** exps[:, None, None]))
-    c.v_absmax.copy_(torch.from_numpy(full.view(np.int16)).view(torch.bfloat16))
-    Q = bf16(rng.standard_normal((2, 4, dim))).cuda()
+    absmax = getattr(c, side + "_absmax")
+    full = bits(absmax).copy()
+    full[page, :, slot] = bits(bf16(nf4.bf16_to_f64(full[page, :, slot]) * 2.0 ** exps[:, None, None]))
+    absmax.copy_(torch.from_numpy(full.view(np.int16)).view(torch.bfloat16))
+    k, v = mirror[0]
+    if side == "k":
+        k = k * 2.0 ** exps[:, None, None]
+    else:
+        v = v * 2.0 ** exps[:, None, None]
+    Q = bf16(rng.standard_normal((n, 4, dim))).cuda()
     out = a.qlora_kv_attention(c, case.batch(a), Q)
     _verify(case, {0: (k, v)}, Q, out, dim ** -0.5, True, 0, "nf4")
 
 
+@pytest.mark.parametrize("n", [2, 60])
 @pytest.mark.parametrize("dim", [64, 128, 256])
-def test_values_of_any_size(dim):
-    _values_of_any_size(dim, hidden=False)
-    _values_of_any_size(dim, hidden=True)
+def test_values_of_any_size(dim, n):
+    """Constants of the values far apart: from 2^-100 to 1, and a token of 2^100 that all rows but the
+    last may not see; all of them huge, tiny, zero; a few binades apart."""
+    rng = np.random.default_rng(51)
+    exps = rng.integers(-100, 0, 90)
+    exps[[3, 88]] = -100
+    _constants_of_any_size(dim, n, "v", exps)
+    exps[89] = 100
+    _constants_of_any_size(dim, n, "v", exps)
+    for e in (-125, -100, 100, 118, -400):
+        _constants_of_any_size(dim, n, "v", np.full(90, e))
+    _constants_of_any_size(dim, n, "v", rng.integers(-9, 1, 90))
 
 
+@pytest.mark.parametrize("n", [2, 60])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_keys_of_any_size(dim, n):
+    """Constants of the keys far apart (a huge key hidden from all rows but the last), zero, tiny."""
+    rng = np.random.default_rng(52)
+    _constants_of_any_size(dim, n, "k", rng.integers(-60, 1, 90))
+    exps = rng.integers(-3, 1, 90)
+    exps[89] = 60
+    _constants_of_any_size(dim, n, "k", exps)
+    for e in (-125, -400):
+        _constants_of_any_size(dim, n, "k", np.full(90, e))
+    _constants_of_any_size(dim, n, "k", rng.integers(-13, 1, 90))
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("n,group", [(2, 4), (40, 8)])
-def test_nan_stays_where_it_is_seen(n, group):
+def test_nan_stays_where_it_is_seen(n, group, dim):
     """A NaN key makes exactly the rows that see it NaN, a NaN value constant its 64 channels of those
-    rows; NaN in a query its own row."""
+    rows; NaN in a query its own row.  Everything else stays within its bound."""
     a = api()
     rng = np.random.default_rng(60)
     case = Case([n, 1], [150, 100], page_size=16, seed=9)
-    heads, dim = 2, 128
+    heads, scale = 2, dim ** -0.5
     c, mirror = filled_cache(a, case, heads, dim, "nf4", rng)
     Q = bf16(rng.standard_normal((case.tokens, heads * group, dim)))
-    ref = a.qlora_kv_attention(c, case.batch(a), Q.cuda()).cpu()
+
+    def check(got, nan):
+        assert torch.equal(torch.isnan(got.float()), nan)
+        for b in range(2):
+            rows = slice(int(case.start[b]), int(case.start[b + 1]))
+            want, bound = kv.attention(f64(Q[rows]), *mirror[b], scale, True, 0, True)
+            far = np.abs(f64(got[rows]) - want) - bound
+            assert far[~nan[rows].numpy()].max() <= 0
+
     last = case.table[0, 149 // 16], 149 % 16  # the last position: row n - 1 alone sees it
-    for side, block in (("k", 0), ("v", 1)):
+    for side, block in (("k", 0), ("v", dim // 64 - 1)):
         absmax = getattr(c, side + "_absmax")
         keep = absmax.clone()
         absmax[last[0], 1, last[1], block] = float("nan")
         got = a.qlora_kv_attention(c, case.batch(a), Q.cuda()).cpu()
-        nan = torch.isnan(got.float())
-        want = torch.zeros_like(nan)
-        want[n - 1, group:, (64 if side == "v" else 0):] = True
-        assert torch.equal(nan, want), side
-        assert torch.equal(got[~want], ref[~want]), side
+        nan = torch.zeros(got.shape, dtype=torch.bool)
+        nan[n - 1, group:, (64 * block if side == "v" else 0):] = True
+        check(got, nan)
         absmax.copy_(keep)
     for poison in (float("nan"), float("inf")):
         Q2 = Q.clone()
         Q2[0, 1, 17] = poison
         got = a.qlora_kv_attention(c, case.batch(a), Q2.cuda()).cpu()
-        want = torch.zeros(got.shape, dtype=torch.bool)
-        want[0, 1] = True
-        assert torch.equal(torch.isnan(got.float()), want)
-        assert torch.equal(got[~want], ref[~want])
+        nan = torch.zeros(got.shape, dtype=torch.bool)
+        nan[0, 1] = True
+        check(got, nan)
 
 
 def test_strided_queries_and_error_free_padding():

@@ -706,7 +706,7 @@ cudaError_t run_attention(KvAttnArgs a, void *ws, int num_sms, cudaStream_t st) 
   a.part_o = reinterpret_cast<float *>(w);
   e = launch_k(k_kv_attention<C>, dim3(num_sms), dim3(C::THREADS), C::SMEM_BYTES, st, 1, a);
   if (e != cudaSuccess) return e;
-  return launch_k(k_kv_join<C::D, C::ROWS, 1>, dim3(workers - 1, C::ROWS), dim3(128), 0, st, 1, a);
+  return launch_k(k_kv_join<C::D, C::ROWS, 4>, dim3(workers - 1, C::ROWS / 4), dim3(128), 0, st, 1, a);
 }
 
 template <class C>

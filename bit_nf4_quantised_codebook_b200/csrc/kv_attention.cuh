@@ -80,89 +80,71 @@ template <int N>  // all but the last N groups of this thread's copies have land
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Joins the items that several workers shared.  CTA (k, y): RPC rows of the item that the
-// range of worker k starts inside of, when worker k holds the item's second part.  The parts'
-// weights come first, all at once; then four warps add every fourth part each, eight loads in
-// flight, and their sums are added in order.
+// Joins the items that several workers shared.  CTA (k, y): WARPS rows, one per warp, of the
+// item that the range of worker k starts inside of, when worker k holds the item's second
+// part.  The parts' weights come first, all at once; then the parts, eight loads in flight.
 constexpr int kMaxWorkers = 1024;
-template <int D, int ROWS, int RPC>
-__global__ void __launch_bounds__(128) k_kv_join(const __grid_constant__ KvAttnArgs a) {
+template <int D, int ROWS, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) k_kv_join(const __grid_constant__ KvAttnArgs a) {
   constexpr int V = D / 32;  // channels per lane
-  __shared__ float s_weight[kMaxWorkers];
-  __shared__ float s_acc[4][D];
-  __shared__ float s_red[8];
   pdl_wait();
   pdl_launch_dependents();
   const int k = static_cast<int>(blockIdx.x) + 1;
   const KvPart p = a.parts[k * 2];
   if (!p.joins) return;
+  const int lane = threadIdx.x & 31, r = static_cast<int>(blockIdx.y) * WARPS + (threadIdx.x >> 5);
   const KvSeq q = kv_seq(a.kb, p.b);
-  const int rows = min(q.n * a.group - p.tile * ROWS, (static_cast<int>(blockIdx.y) + 1) * RPC);
-  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  const int rr = p.tile * ROWS + r;
+  if (rr >= q.n * a.group) return;
   const int n = p.last - p.g0 + 1;
   auto part_of = [&](int i) { return static_cast<int64_t>(p.g0 + i) * 2 + (i == 0 ? p.head_slot : 0); };
-  for (int r = blockIdx.y * RPC; r < rows; ++r) {
-    float top = -INFINITY;
-    for (int i = tid; i < n; i += 128) {
-      const int64_t part = part_of(i);
-      const float lse = a.parts[part].present ? a.part_lse[part * ROWS + r] : -INFINITY;  // workers without steps
-      s_weight[i] = lse;
-      top = fmaxf(top, lse);
+  auto lse_of = [&](int i) {
+    const int64_t part = part_of(i);
+    return a.parts[part].present ? a.part_lse[part * ROWS + r] : -INFINITY;  // workers without steps
+  };
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, lse_of(i));
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+  float sum = 0.0f, acc[V] = {};
+  for (int base = 0; base < n; base += 32) {
+    float weight = 0.0f;
+    if (base + lane < n) {
+      const float lse = lse_of(base + lane);
+      weight = lse == -INFINITY ? 0.0f : ex2(lse - top);
     }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    if (lane == 0) s_red[w] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
-    float sum = 0.0f;
-    for (int i = tid; i < n; i += 128) {
-      const float lse = s_weight[i];
-      const float f = lse == -INFINITY ? 0.0f : ex2(lse - top);
-      s_weight[i] = f;
-      sum += f;
-    }
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-    if (lane == 0) s_red[4 + w] = sum;
-    __syncthreads();
-    sum = (s_red[4] + s_red[5]) + (s_red[6] + s_red[7]);
-    float acc[V] = {};
-    auto add = [&](int i, const float2 (&v)[V / 2]) {
-      const float f = s_weight[i];
-      if (f == 0.0f) return;  // an absent part holds anything
-#pragma unroll
-      for (int j = 0; j < V; j += 2) {
-        acc[j] = fmaf(f, v[j / 2].x, acc[j]);
-        acc[j + 1] = fmaf(f, v[j / 2].y, acc[j + 1]);
-      }
-    };
-    auto load = [&](int i, float2 (&v)[V / 2]) {
-      const float *src = a.part_o + (part_of(i) * ROWS + r) * D + lane * V;
-#pragma unroll
-      for (int j = 0; j < V / 2; ++j) v[j] = *reinterpret_cast<const float2 *>(src + 2 * j);
-    };
+    sum += weight;
+    const int here = min(32, n - base);
     constexpr int U = 8;
-    for (int i0 = w; i0 < n; i0 += 4 * U) {
+    for (int j0 = 0; j0 < here; j0 += U) {
       float2 v[U][V / 2];
 #pragma unroll
-      for (int j = 0; j < U; ++j) load(min(i0 + 4 * j, n - 1), v[j]);
+      for (int j = 0; j < U; ++j) {
+        const float *src = a.part_o + (part_of(base + min(j0 + j, here - 1)) * ROWS + r) * D + lane * V;
 #pragma unroll
-      for (int j = 0; j < U; ++j)
-        if (i0 + 4 * j < n) add(i0 + 4 * j, v[j]);
-    }
+        for (int x = 0; x < V / 2; ++x) v[j][x] = *reinterpret_cast<const float2 *>(src + 2 * x);
+      }
 #pragma unroll
-    for (int j = 0; j < V; ++j) s_acc[w][lane * V + j] = acc[j];
-    __syncthreads();
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int rr = p.tile * ROWS + r, i = rr / a.group, h = rr - i * a.group;
-    uint16_t *dst = a.out + (static_cast<int64_t>(q.row0 + i) * a.heads * a.group + p.head * a.group + h) * D;
-    for (int c = tid * 2; c < D; c += 256) {
-      const float x = (s_acc[0][c] + s_acc[1][c]) + (s_acc[2][c] + s_acc[3][c]);
-      const float y = (s_acc[0][c + 1] + s_acc[1][c + 1]) + (s_acc[2][c + 1] + s_acc[3][c + 1]);
-      *reinterpret_cast<uint32_t *>(dst + c) = pack_bf16x2(x * inv, y * inv);
+      for (int j = 0; j < U; ++j) {
+        const float f = __shfl_sync(0xFFFFFFFFu, weight, (j0 + j) & 31);
+        if (j0 + j < here && f != 0.0f) {  // an absent part holds anything
+#pragma unroll
+          for (int x = 0; x < V / 2; ++x) {
+            acc[2 * x] = fmaf(f, v[j][x].x, acc[2 * x]);
+            acc[2 * x + 1] = fmaf(f, v[j][x].y, acc[2 * x + 1]);
+          }
+        }
+      }
     }
-    if (RPC > 1) __syncthreads();  // the shared arrays are free again
   }
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int i = rr / a.group, h = rr - i * a.group;
+  uint16_t *dst = a.out + ((static_cast<int64_t>(q.row0 + i) * a.heads + p.head) * a.group + h) * D + lane * V;
+#pragma unroll
+  for (int x = 0; x < V / 2; ++x)
+    *reinterpret_cast<uint32_t *>(dst + 2 * x) = pack_bf16x2(acc[2 * x] * inv, acc[2 * x + 1] * inv);
 }
 
 // kv_prefill.cu

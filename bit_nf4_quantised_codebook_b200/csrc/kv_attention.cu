@@ -37,6 +37,7 @@
 // memory at the end of its part of an item.  An item that several groups shared is joined
 // from their normalised parts, in order, by a second small kernel.
 #include <atomic>
+#include <climits>
 #include <cstdint>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -706,7 +707,7 @@ cudaError_t run_attention(KvAttnArgs a, void *ws, int num_sms, cudaStream_t st) 
   a.part_o = reinterpret_cast<float *>(w);
   e = launch_k(k_kv_attention<C>, dim3(num_sms), dim3(C::THREADS), C::SMEM_BYTES, st, 1, a);
   if (e != cudaSuccess) return e;
-  return launch_k(k_kv_join<C::D, C::ROWS, 4>, dim3(workers - 1, C::ROWS / 4), dim3(128), 0, st, 1, a);
+  return launch_k(k_kv_join<C::D, C::ROWS, 2, 4>, dim3(workers - 1, C::ROWS / 2), dim3(256), 0, st, 1, a);
 }
 
 template <class C>
@@ -727,11 +728,18 @@ size_t few_workspace(int head_dim, int num_sms) {
 // Sequences with more rows (tokens x query heads per key/value head) than this go to the
 // many-row kernel.
 constexpr int kFewRows = 64;
+// The host does not know how a call's rows are spread.  If every sequence has one token or
+// more, none has more than tokens - batch + 1: up to that many rows above one token each, the
+// few-row kernel takes the whole call (right for any number of rows, each 16 of them decoding
+// the cache anew).  Measured: the many-row kernel's launches cost a call without use for them
+// 11 us (64 single tokens over 2800 on average, 8 rows each: 117 against 128 us).
+constexpr int64_t kSpreadRows = 512;
+bool may_have_many_rows(int64_t tokens, int batch, int group) { return (tokens - batch) * group > kSpreadRows; }
 }  // namespace
 
 size_t kv_attention_workspace(int head_dim, int group, int batch, int64_t tokens, int num_sms) {
   size_t bytes = (few_workspace(head_dim, num_sms) + 15) / 16 * 16;
-  if (tokens * group > kFewRows) bytes += kv_prefill_workspace(head_dim, group, batch, tokens, num_sms);
+  if (may_have_many_rows(tokens, batch, group)) bytes += kv_prefill_workspace(head_dim, group, batch, tokens, num_sms);
   return bytes;
 }
 
@@ -762,8 +770,9 @@ cudaError_t launch_kv_attention(const qlora_kv_cache &c, const KvBatch &kb, cons
   a.v_unit = 1.0f / unit;
   a.causal = causal;
   a.window = window;
-  a.few_rows = kFewRows;
-  if (static_cast<int64_t>(kb.tokens) * a.group > kFewRows) {  // some sequence may have many rows
+  a.few_rows = INT_MAX;
+  if (may_have_many_rows(kb.tokens, kb.batch, a.group)) {
+    a.few_rows = kFewRows;
     uint8_t *more = static_cast<uint8_t *>(ws) + (few_workspace(c.head_dim, num_sms) + 15) / 16 * 16;
     const cudaError_t e = launch_kv_prefill(a, c.head_dim, more, num_sms, timeout_ns, st);
     if (e != cudaSuccess) return e;

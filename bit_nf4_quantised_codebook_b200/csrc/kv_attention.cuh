@@ -80,23 +80,26 @@ template <int N>  // all but the last N groups of this thread's copies have land
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Joins the items that several workers shared.  CTA (k, y): WARPS rows, one per warp, of the
+// Joins the items that several workers shared.  CTA (k, y): WARPS rows, SPLIT warps to each, of the
 // item that the range of worker k starts inside of, when worker k holds the item's second
 // part.  The parts' weights come first, all at once; then the parts, eight loads in flight.
 constexpr int kMaxWorkers = 1024;
-template <int D, int ROWS, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) k_kv_join(const __grid_constant__ KvAttnArgs a) {
+template <int D, int ROWS, int WARPS, int SPLIT>
+__global__ void __launch_bounds__(WARPS * SPLIT * 32) k_kv_join(const __grid_constant__ KvAttnArgs a) {
   constexpr int V = D / 32;  // channels per lane
+  __shared__ float s_acc[SPLIT > 1 ? WARPS * SPLIT * D : 1];
   pdl_wait();
   pdl_launch_dependents();
   const int k = static_cast<int>(blockIdx.x) + 1;
   const KvPart p = a.parts[k * 2];
   if (!p.joins) return;
-  const int lane = threadIdx.x & 31, r = static_cast<int>(blockIdx.y) * WARPS + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp % SPLIT;
+  const int r = static_cast<int>(blockIdx.y) * WARPS + warp / SPLIT;
   const KvSeq q = kv_seq(a.kb, p.b);
   const int rr = p.tile * ROWS + r;
-  if (rr >= q.n * a.group) return;
-  const int n = p.last - p.g0 + 1;
+  const bool live = rr < q.n * a.group;
+  if (SPLIT == 1 && !live) return;
+  const int n = live ? p.last - p.g0 + 1 : 0;
   auto part_of = [&](int i) { return static_cast<int64_t>(p.g0 + i) * 2 + (i == 0 ? p.head_slot : 0); };
   auto lse_of = [&](int i) {
     const int64_t part = part_of(i);
@@ -107,20 +110,26 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv_join(const __grid_constant__ 
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
   float sum = 0.0f, acc[V] = {};
-  for (int base = 0; base < n; base += 32) {
+  // this warp's parts: share, share + SPLIT, ...
+  const int mine = (n - share + SPLIT - 1) / SPLIT;
+  for (int i = lane; i < n; i += 32) {
+    const float lse = lse_of(i);
+    sum += lse == -INFINITY ? 0.0f : ex2(lse - top);
+  }
+  for (int base = 0; base < mine; base += 32) {
     float weight = 0.0f;
-    if (base + lane < n) {
-      const float lse = lse_of(base + lane);
+    if (base + lane < mine) {
+      const float lse = lse_of(share + (base + lane) * SPLIT);
       weight = lse == -INFINITY ? 0.0f : ex2(lse - top);
     }
-    sum += weight;
-    const int here = min(32, n - base);
+    const int here = min(32, mine - base);
     constexpr int U = 8;
     for (int j0 = 0; j0 < here; j0 += U) {
       float2 v[U][V / 2];
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const float *src = a.part_o + (part_of(base + min(j0 + j, here - 1)) * ROWS + r) * D + lane * V;
+        const int i = share + (base + min(j0 + j, here - 1)) * SPLIT;
+        const float *src = a.part_o + (part_of(i) * ROWS + r) * D + lane * V;
 #pragma unroll
         for (int x = 0; x < V / 2; ++x) v[j][x] = *reinterpret_cast<const float2 *>(src + 2 * x);
       }
@@ -139,6 +148,16 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv_join(const __grid_constant__ 
   }
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+  if (SPLIT > 1) {  // the row's warps, in order
+#pragma unroll
+    for (int x = 0; x < V; ++x) s_acc[warp * D + lane * V + x] = acc[x];
+    __syncthreads();
+    if (share != 0 || !live) return;
+#pragma unroll
+    for (int w = 1; w < SPLIT; ++w)
+#pragma unroll
+      for (int x = 0; x < V; ++x) acc[x] += s_acc[(warp + w) * D + lane * V + x];
+  }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   const int i = rr / a.group, h = rr - i * a.group;
   uint16_t *dst = a.out + ((static_cast<int64_t>(q.row0 + i) * a.heads + p.head) * a.group + h) * D + lane * V;

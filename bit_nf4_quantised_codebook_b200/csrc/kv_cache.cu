@@ -3,11 +3,11 @@
 // LLMs" (intuitivepapers.ai, §Quantize in blocks, §NormalFloat) with blocks of 64
 // channels and the block's absmax kept, in bfloat16, where it is exact.
 //
-// Both kernels stream: a token's key and value of every head are a row of 8-channel
-// units (16 bytes of bfloat16, 4 bytes of codes); a CTA takes up to 1024 units - whole
-// token rows, or a piece of one - finds the cache slot of each of its token rows once
-// (binary search over token_start, then the page table), and each thread then moves
-// four units, their loads issued together.
+// Both kernels stream: a token's row is a run of 8-channel units (16 bytes of bfloat16, 4
+// bytes of codes), the same for its key and its value.  A CTA takes up to 512 units - whole
+// token rows, or a piece of one - finds the cache row of each of its tokens once (one guess,
+// or a binary search over token_start, then the page table), and each thread then moves two
+// units of both sides, all loads issued together.
 // Bound by HBM for prompts (2 + 17/32 bytes per element each way) and by the chain of
 // dependent loads token_start -> kv_len -> page_table -> data for single tokens.
 //
@@ -33,9 +33,10 @@ namespace qlora {
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr int kKvUnitsPerThread = 4;
-constexpr int kKvSpan = kKvThreads * kKvUnitsPerThread;  // units of one CTA
-constexpr int kKvMaxTokens = kKvSpan / 8;                // token rows of one CTA (>= 8 units each)
+constexpr int kKvUnits = 2;                      // units of a thread
+constexpr int kKvSpan = kKvThreads * kKvUnits;   // units of a CTA
+constexpr int kKvMaxTokens = kKvSpan / 8;        // token rows of a CTA (8 units or more each)
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;
 
 struct KvCodeTable {
   uint32_t e[32];
@@ -49,25 +50,22 @@ struct KvRows {
   uint16_t *absmax[2];
   int heads;
   int head_shift;       // a head is 1 << head_shift units
-  int per_side;         // units of a token's keys: heads << head_shift
-  int per_token;        // per_side, times 2 unless one output is not wanted
+  int per_token;        // units of a token: heads << head_shift
   int tokens_per_cta;   // whole token rows of a CTA; 1 when a row is split over blockIdx.y
   uint32_t magic;       // ceil(2^32 / per_token): w / per_token = umulhi(w, magic) for w * per_token < 2^32
 };
 
-// Unit v of this CTA: its token row (counted from the CTA's first), side, head and
-// place in the head.  False when there is no such unit.
+// Unit v of this CTA: its token row (counted from the CTA's first), and place in it.
+// False when there is no such unit.
 struct KvUnit {
-  int t, side, head, sub;
+  int t, in_row, head, sub;
 };
 __device__ __forceinline__ bool kv_unit(const KvRows &r, int v, int rows, KvUnit &u) {
   const int w = static_cast<int>(blockIdx.y) * kKvSpan + v;
   u.t = static_cast<int>(__umulhi(static_cast<uint32_t>(w), r.magic));
-  const int x = w - u.t * r.per_token;
-  u.side = x >= r.per_side ? 1 : 0;
-  const int y = x - u.side * r.per_side;
-  u.head = y >> r.head_shift;
-  u.sub = y - (u.head << r.head_shift);
+  u.in_row = w - u.t * r.per_token;
+  u.head = u.in_row >> r.head_shift;
+  u.sub = u.in_row - (u.head << r.head_shift);
   return u.t < rows;
 }
 
@@ -79,40 +77,37 @@ __device__ __forceinline__ uint4 ld_stream(const void *p) {
   return v;
 }
 
-// Slot index page * page_size + slot (a 64-bit value) of token row t, or -1 when no
-// sequence owns the row or its position or page is out of range.
-__device__ __forceinline__ int64_t row_slot(const KvBatch &kb, int t) {
-  int lo = 0, hi = kb.batch;  // last b in [0, batch) with token_start[b] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(kb.token_start + mid) <= t) lo = mid;
-    else hi = mid;
+// Cache row of head 0 of token row t (rows count (page, head, slot) in that order: below
+// 2^31), or kNoRow when no sequence owns the row or its position or page is out of range.
+__device__ __forceinline__ uint32_t token_row(const KvBatch &kb, int heads, int t) {
+  // the sequence: with one token each it is t; else the last one with token_start <= t
+  int lo = min(t, kb.batch - 1);
+  if (!(__ldg(kb.token_start + lo) <= t && t < __ldg(kb.token_start + lo + 1))) {
+    lo = 0;
+    for (int hi = kb.batch; hi - lo > 1;) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(kb.token_start + mid) <= t) lo = mid;
+      else hi = mid;
+    }
   }
   const KvSeq q = kv_seq(kb, lo);
   const int i = t - q.row0;
-  if (i < 0 || i >= q.n) return -1;
+  if (i < 0 || i >= q.n) return kNoRow;
   const int p = q.pos0() + i;
   const int page = p < 0 ? -1 : kv_page(kb, lo, p);
   if (page < 0) {
     kv_error(kb);
-    return -1;
+    return kNoRow;
   }
-  return (static_cast<int64_t>(page) << kb.page_shift) | (p & ((1 << kb.page_shift) - 1));
+  return ((static_cast<uint32_t>(page) * heads) << kb.page_shift) + (p & ((1 << kb.page_shift) - 1));
 }
 
-// The slots of this CTA's token rows, into shared memory; returns how many rows.
-__device__ __forceinline__ int load_slots(const KvBatch &kb, int t0, int per_cta, int64_t *slots) {
-  const int rows = min(per_cta, kb.tokens - t0);
-  for (int i = threadIdx.x; i < rows; i += kKvThreads) slots[i] = row_slot(kb, t0 + i);
+// The cache rows of this CTA's tokens, into shared memory; returns how many tokens.
+__device__ __forceinline__ int load_rows(const KvBatch &kb, const KvRows &r, int t0, uint32_t *rows) {
+  const int n = min(r.tokens_per_cta, kb.tokens - t0);
+  for (int i = threadIdx.x; i < n; i += kKvThreads) rows[i] = token_row(kb, r.heads, t0 + i);
   __syncthreads();
-  return rows;
-}
-
-// Flat index of a slot and head in the cache's [page][head][slot] order.
-__device__ __forceinline__ int64_t cache_row(const KvBatch &kb, int64_t slot, int head, int heads) {
-  const int64_t page = slot >> kb.page_shift;
-  const int in_page = static_cast<int>(slot) & ((1 << kb.page_shift) - 1);
-  return ((page * heads + head) << kb.page_shift) + in_page;
+  return n;
 }
 
 // LOG: buckets by sign and exponent (E3M0, one threshold per binade); otherwise 31
@@ -134,113 +129,139 @@ __device__ __forceinline__ uint32_t kv_code(float x, const uint32_t *tab) {
   return SKIP8 && c == 8u ? 9u : c;
 }
 
+// Codes of the 8 elements of `raw`, whose block the 8 neighbouring lanes share; `m` becomes the
+// block's absmax as bfloat16 bits.
+template <bool LOG, bool SKIP8>
+__device__ __forceinline__ uint32_t kv_encode(const uint4 &raw, const uint32_t *tab, uint32_t &m) {
+  const uint32_t wd[4] = {raw.x, raw.y, raw.z, raw.w};
+  // the bits of non-negative values order like integers, infinities and NaN above every finite one
+  m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, wd[i] & 0x7FFF7FFFu);
+  m = max(m >> 16, m & 0xFFFFu);
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+  m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(wd[i] << 16);
+    x[2 * i + 1] = __uint_as_float(wd[i] & 0xFFFF0000u);
+  }
+  float c = __uint_as_float(m << 16);
+  if (m < (31u << 7) || m >= (223u << 7)) {
+    // very small and very large blocks are scaled by 2^96 or 2^-96, exactly, so that the
+    // reciprocal is a normal number
+    const float scale = m < (31u << 7) ? 0x1p96f : 0x1p-96f;
+    c *= scale;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= scale;
+  }
+  const float rc = c > 0.0f ? __frcp_rn(c) : 0.0f;  // a zero block: every ratio 0
+  uint32_t packed = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t hi = kv_code<LOG, SKIP8>(__fmul_rn(x[2 * i], rc), tab);
+    const uint32_t lo = kv_code<LOG, SKIP8>(__fmul_rn(x[2 * i + 1], rc), tab);
+    packed += (hi * 16u + lo) << (8 * i);
+  }
+  return packed;
+}
+
 template <bool LOG, bool SKIP8>
 __global__ void __launch_bounds__(kKvThreads) k_kv_append(const __grid_constant__ KvBatch kb,
                                                            const __grid_constant__ KvRows r,
                                                            const __grid_constant__ KvCodeTable table) {
   __shared__ uint32_t s_tab[32];
-  __shared__ int64_t s_slot[kKvMaxTokens];
+  __shared__ uint32_t s_row[kKvMaxTokens];
   if (threadIdx.x < 32) s_tab[threadIdx.x] = table.e[threadIdx.x];
   pdl_wait();
   pdl_launch_dependents();
   const int t0 = static_cast<int>(blockIdx.x) * r.tokens_per_cta;
-  const int rows = load_slots(kb, t0, r.tokens_per_cta, s_slot);
-
-  uint4 raw[kKvUnitsPerThread];
-  int64_t row[kKvUnitsPerThread];
-  int side[kKvUnitsPerThread], sub[kKvUnitsPerThread];
+  const int n = load_rows(kb, r, t0, s_row);
+  uint4 raw[kKvUnits][2];
+  uint32_t row[kKvUnits], sub[kKvUnits];
 #pragma unroll
-  for (int k = 0; k < kKvUnitsPerThread; ++k) {
+  for (int k = 0; k < kKvUnits; ++k) {
     KvUnit u;
-    row[k] = -1;
-    raw[k] = make_uint4(0, 0, 0, 0);
-    if (kv_unit(r, k * kKvThreads + threadIdx.x, rows, u) && s_slot[u.t] >= 0) {
-      row[k] = cache_row(kb, s_slot[u.t], u.head, r.heads);
-      raw[k] = ld_stream(r.src[u.side] + static_cast<int64_t>(t0 + u.t) * r.token_stride[u.side] +
-                         static_cast<int64_t>(u.head) * r.head_stride[u.side] + u.sub * 8);
+    row[k] = kNoRow;
+    raw[k][0] = raw[k][1] = make_uint4(0, 0, 0, 0);
+    if (kv_unit(r, k * kKvThreads + threadIdx.x, n, u) && s_row[u.t] != kNoRow) {
+      row[k] = s_row[u.t] + (static_cast<uint32_t>(u.head) << kb.page_shift);
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        raw[k][s] = ld_stream(r.src[s] + static_cast<int64_t>(t0 + u.t) * r.token_stride[s] +
+                              static_cast<int64_t>(u.head) * r.head_stride[s] + u.sub * 8);
     }
-    side[k] = u.side;
     sub[k] = u.sub;
   }
   bool bad = false;
 #pragma unroll
-  for (int k = 0; k < kKvUnitsPerThread; ++k) {
-    const uint32_t wd[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-    // largest magnitude of the 8 elements, as bfloat16 bits: those of non-negative
-    // values order like integers, infinities and NaN above every finite one
-    uint32_t m = 0;
+  for (int k = 0; k < kKvUnits; ++k)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = __vmaxu2(m, wd[i] & 0x7FFF7FFFu);
-    m = max(m >> 16, m & 0xFFFFu);
-    // the 8 threads of a block are consecutive lanes (units come in whole heads)
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-    m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-    const bool finite = m < 0x7F80u;
-    float c = __uint_as_float(m << 16), scale = 1.0f;
-    // very small and very large blocks are scaled by 2^96 or 2^-96, exactly, so that the
-    // reciprocal is a normal number
-    if (m < (31u << 7)) scale = 0x1p96f;
-    if (m >= (223u << 7)) scale = 0x1p-96f;
-    c *= scale;
-    const float rc = c > 0.0f && finite ? __frcp_rn(c) : 0.0f;  // zero and non-finite blocks: every ratio 0
-    uint32_t packed = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float lo = __uint_as_float(wd[i] << 16), hi = __uint_as_float(wd[i] & 0xFFFF0000u);
-      lo = finite ? __fmul_rn(__fmul_rn(lo, scale), rc) : 0.0f;
-      hi = finite ? __fmul_rn(__fmul_rn(hi, scale), rc) : 0.0f;
-      packed |= ((kv_code<LOG, SKIP8>(lo, s_tab) << 4) | kv_code<LOG, SKIP8>(hi, s_tab)) << (8 * i);
+    for (int s = 0; s < 2; ++s) {
+      uint32_t m;  // (units come in whole heads: 8 lanes share a block)
+      const uint32_t packed = kv_encode<LOG, SKIP8>(raw[k][s], s_tab, m);
+      if (row[k] != kNoRow) {
+        reinterpret_cast<uint32_t *>(r.codes[s])[(static_cast<uint64_t>(row[k]) << r.head_shift) + sub[k]] = packed;
+        const bool finite = m < 0x7F80u;
+        if ((sub[k] & 7) == 0)
+          r.absmax[s][(static_cast<uint64_t>(row[k]) << (r.head_shift - 3)) + (sub[k] >> 3)] =
+              static_cast<uint16_t>(finite ? m : 0x7FC0u);
+        bad |= !finite;
+      }
     }
-    if (row[k] >= 0) {
-      const int s = side[k];
-      reinterpret_cast<uint32_t *>(r.codes[s])[(row[k] << r.head_shift) + sub[k]] = packed;
-      if ((sub[k] & 7) == 0)
-        r.absmax[s][(row[k] << (r.head_shift - 3)) + (sub[k] >> 3)] = static_cast<uint16_t>(finite ? m : 0x7FC0u);
-      bad |= !finite;
-    }
-  }
   if (bad && kb.dev_err) atomicOr(kb.dev_err, QLORA_DEVERR_NONFINITE);
 }
 
+// KEYS, VALUES: which sides are wanted.
+template <bool KEYS, bool VALUES>
 __global__ void __launch_bounds__(kKvThreads) k_kv_read(const __grid_constant__ KvBatch kb,
                                                          const __grid_constant__ KvRows r,
                                                          const __grid_constant__ Nf4Levels lv) {
   __shared__ float s_level[16];  // 16 words in 16 banks: a lookup never conflicts
-  __shared__ int64_t s_slot[kKvMaxTokens];
+  __shared__ uint32_t s_row[kKvMaxTokens];
   if (threadIdx.x < 16) s_level[threadIdx.x] = lv.q[threadIdx.x];
   pdl_wait();
   pdl_launch_dependents();
   const int t0 = static_cast<int>(blockIdx.x) * r.tokens_per_cta;
-  const int rows = load_slots(kb, t0, r.tokens_per_cta, s_slot);
-
-  uint32_t codes[kKvUnitsPerThread], amax[kKvUnitsPerThread];
-  uint16_t *dst[kKvUnitsPerThread];
+  const int n = load_rows(kb, r, t0, s_row);
+  uint32_t codes[kKvUnits][2], amax[kKvUnits][2];
+  int64_t dst[kKvUnits];  // unit of the outputs, or -1
 #pragma unroll
-  for (int k = 0; k < kKvUnitsPerThread; ++k) {
+  for (int k = 0; k < kKvUnits; ++k) {
     KvUnit u;
-    dst[k] = nullptr;
-    codes[k] = amax[k] = 0;
-    if (kv_unit(r, k * kKvThreads + threadIdx.x, rows, u) && s_slot[u.t] >= 0) {
-      const int64_t row = cache_row(kb, s_slot[u.t], u.head, r.heads);
-      codes[k] = __ldg(reinterpret_cast<const uint32_t *>(r.codes[u.side]) + (row << r.head_shift) + u.sub);
-      amax[k] = __ldg(r.absmax[u.side] + (row << (r.head_shift - 3)) + (u.sub >> 3));
-      dst[k] = r.dst[u.side] + (((static_cast<int64_t>(t0 + u.t) * r.heads + u.head) << r.head_shift) + u.sub) * 8;
+    dst[k] = -1;
+    codes[k][0] = codes[k][1] = amax[k][0] = amax[k][1] = 0;
+    if (kv_unit(r, k * kKvThreads + threadIdx.x, n, u) && s_row[u.t] != kNoRow) {
+      const uint64_t row = s_row[u.t] + (static_cast<uint32_t>(u.head) << kb.page_shift);
+      const uint64_t at = (row << r.head_shift) + u.sub, block = (row << (r.head_shift - 3)) + (u.sub >> 3);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (!(s == 0 ? KEYS : VALUES)) continue;
+        codes[k][s] = __ldg(reinterpret_cast<const uint32_t *>(r.codes[s]) + at);
+        amax[k][s] = __ldg(r.absmax[s] + block);
+      }
+      dst[k] = static_cast<int64_t>(t0 + u.t) * r.per_token + u.in_row;
     }
   }
 #pragma unroll
-  for (int k = 0; k < kKvUnitsPerThread; ++k) {
-    const float c = __uint_as_float(amax[k] << 16);
-    uint32_t o[4];
+  for (int k = 0; k < kKvUnits; ++k)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = pack_bf16x2(__fmul_rn(s_level[(codes[k] >> (8 * i + 4)) & 15u], c),
-                         __fmul_rn(s_level[(codes[k] >> (8 * i)) & 15u], c));
-    if (dst[k]) *reinterpret_cast<uint4 *>(dst[k]) = make_uint4(o[0], o[1], o[2], o[3]);
-  }
+    for (int s = 0; s < 2; ++s) {
+      if (!(s == 0 ? KEYS : VALUES)) continue;
+      const float c = __uint_as_float(amax[k][s] << 16);
+      uint32_t o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = pack_bf16x2(__fmul_rn(s_level[(codes[k][s] >> (8 * i + 4)) & 15u], c),
+                           __fmul_rn(s_level[(codes[k][s] >> (8 * i)) & 15u], c));
+      if (dst[k] >= 0)
+        __stcs(reinterpret_cast<uint4 *>(r.dst[s]) + dst[k], make_uint4(o[0], o[1], o[2], o[3]));
+    }
 }
 
-KvRows cache_rows(const qlora_kv_cache &c, int sides) {
+KvRows cache_rows(const qlora_kv_cache &c) {
   KvRows r = {};
   r.codes[0] = c.k_codes;
   r.codes[1] = c.v_codes;
@@ -248,8 +269,7 @@ KvRows cache_rows(const qlora_kv_cache &c, int sides) {
   r.absmax[1] = c.v_absmax;
   r.heads = c.heads;
   r.head_shift = c.head_dim == 64 ? 3 : c.head_dim == 128 ? 4 : 5;
-  r.per_side = c.heads << r.head_shift;
-  r.per_token = sides * r.per_side;
+  r.per_token = c.heads << r.head_shift;
   r.tokens_per_cta = r.per_token < kKvSpan ? kKvSpan / r.per_token : 1;
   r.magic = static_cast<uint32_t>(((1ull << 32) + r.per_token - 1) / r.per_token);
   return r;
@@ -361,7 +381,7 @@ bool build_kv_code_table(int codebook, uint32_t table[32]) {
 cudaError_t launch_kv_append(const qlora_kv_cache &c, const KvBatch &kb, const uint16_t *K, int64_t k_token_stride,
                              int64_t k_head_stride, const uint16_t *V, int64_t v_token_stride, int64_t v_head_stride,
                              const uint32_t table[32], cudaStream_t st) {
-  KvRows r = cache_rows(c, 2);
+  KvRows r = cache_rows(c);
   r.src[0] = K;
   r.src[1] = V;
   r.token_stride[0] = k_token_stride;
@@ -380,17 +400,15 @@ cudaError_t launch_kv_append(const qlora_kv_cache &c, const KvBatch &kb, const u
 
 cudaError_t launch_kv_read(const qlora_kv_cache &c, const KvBatch &kb, uint16_t *K_out, uint16_t *V_out,
                            const float levels[16], cudaStream_t st) {
-  KvRows r = cache_rows(c, K_out && V_out ? 2 : 1);
+  KvRows r = cache_rows(c);
   r.dst[0] = K_out;
   r.dst[1] = V_out;
-  if (!K_out) {  // the values alone
-    r.dst[0] = V_out;
-    r.codes[0] = c.v_codes;
-    r.absmax[0] = c.v_absmax;
-  }
   Nf4Levels lv;
   std::memcpy(lv.q, levels, sizeof(lv.q));
-  return launch_k(k_kv_read, rows_grid(r, kb.tokens), dim3(kKvThreads), 0, st, 1, kb, r, lv);
+  const dim3 grid = rows_grid(r, kb.tokens);
+  if (!K_out) return launch_k(k_kv_read<false, true>, grid, dim3(kKvThreads), 0, st, 1, kb, r, lv);
+  if (!V_out) return launch_k(k_kv_read<true, false>, grid, dim3(kKvThreads), 0, st, 1, kb, r, lv);
+  return launch_k(k_kv_read<true, true>, grid, dim3(kKvThreads), 0, st, 1, kb, r, lv);
 }
 
 }  // namespace qlora

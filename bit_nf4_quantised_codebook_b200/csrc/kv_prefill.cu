@@ -984,7 +984,7 @@ cudaError_t run_prefill(const KvAttnArgs &args, void *ws, int num_sms, unsigned 
   p.a.part_o = reinterpret_cast<float *>(w);
   if ((e = launch_k(k_kv_plan<C>, dim3(1), dim3(kPlanThreads), 0, st, 1, p)) != cudaSuccess) return e;
   if ((e = launch_k(k_kv_prefill<C>, dim3(num_sms), dim3(C::THREADS), C::SMEM_BYTES, st, 1, p)) != cudaSuccess) return e;
-  return launch_k(k_kv_join<C::D, C::ROWS, 8>, dim3(num_sms - 1, C::ROWS / 8), dim3(256), 0, st, 1, p.a);
+  return launch_k(k_kv_join<C::D, C::ROWS, 8, 1>, dim3(num_sms - 1, C::ROWS / 8), dim3(256), 0, st, 1, p.a);
 }
 
 }  // namespace

@@ -19,7 +19,8 @@
 // P^T is S^T's accumulator transposed with movmatrix.
 //
 // Numbers.  Levels are held in fp16: exactly for the integer and float grids (stored as
-// the small integers they are multiples of), within 2^-12 for NF4.  Each query row is
+// the small integers they are multiples of), within 2^-11 for NF4, at a scale where their
+// errors cancel on average (see launch_kv_attention).  Each query row is
 // scaled by a power of two to a largest magnitude in [2^13, 2^14) and is then exact in
 // fp16 down to 2^-38 of it.  The softmax keeps a reference m per row (its running maximum
 // when last renewed) and float32 weights P = 2^(s - m) and their sum.  Into the second
@@ -109,6 +110,14 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs &a, int b, int tile_r
   return s;
 }
 
+// What a warp needs again after the steps of a part.  Kept in shared memory meanwhile: with
+// little first-level cache beside it, a spilled register would be a second-level cache access
+// in every step.
+struct WarpState {
+  int64_t at, stop, begin, total, seq_start, first, end;
+  int b, head, tile, step0, step1, row0, n, len, tiles, steps, lo;
+};
+
 template <int D_, int NT_, int GROUPS_>
 struct AttnCfg {
   static constexpr int D = D_;
@@ -117,18 +126,18 @@ struct AttnCfg {
   static constexpr int NB = D / 64;       // blocks of 64 channels
   static constexpr int GROUPS = GROUPS_;  // warp groups per CTA
   static constexpr int THREADS = GROUPS * 128;
-  static constexpr int T = D == 256 ? 1 : 2;  // tiles of 16 tokens in one part of a warp's work
+  static constexpr int T = D * NT > 128 ? 1 : 2;  // tiles of 16 tokens in one part of a warp's work
   static constexpr int PARTS = 2 / T;         // parts of a warp's 32 tokens of a step
   static constexpr int CW = (NB + 1) / 2;     // words of a token's constants
   // shared memory: a ring of parts per warp, the first FRONT of them before the table
   static constexpr int CODES = T * 16 * (D / 2), CONSTS = T * 16 * NB * 2;  // bytes of a part's keys (values the same)
   static constexpr int PART_BYTES = 2 * (CODES + CONSTS);
-  static constexpr int STAGES = D == 64 ? 4 : 2;
+  static constexpr int STAGES = 8704 / PART_BYTES;  // 2 or 4
   static constexpr int RING = STAGES * PART_BYTES;
   static constexpr int WARPS = 4 * GROUPS;
   static constexpr int FRONT = 7;
   static constexpr int LSE_BYTES = WARPS * ROWS * 4;
-  static constexpr int SMEM_BYTES = 0x20000 + (WARPS - FRONT) * RING + LSE_BYTES + (THREADS + 1) * 8;
+  static constexpr int SMEM_BYTES = 0x20000 + (WARPS - FRONT) * RING + LSE_BYTES + (THREADS + 1) * 8 + WARPS * sizeof(WarpState);
   static_assert(ROWS * D * 4 <= RING, "a warp's outputs are joined in its ring");
   static_assert(RING % 128 == 0 && FRONT * RING <= 0x10000 - 0x400, "rings before the table");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
@@ -154,6 +163,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
   uint8_t *tail = smem + (table - smem_base) + 0x10000u;    // rings, the joins' sums, the line's prefix sums
   float *lse = reinterpret_cast<float *>(tail + (C::WARPS - C::FRONT) * C::RING);
   int64_t *prefix = reinterpret_cast<int64_t *>(tail + (C::WARPS - C::FRONT) * C::RING + C::LSE_BYTES);
+  volatile WarpState *state = reinterpret_cast<WarpState *>(prefix + C::THREADS + 1) + (threadIdx.x >> 5);
   __shared__ int64_t s_warp_sum[C::THREADS / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = warp >> 2, gw = warp & 3;  // group in the CTA, warp in the group
@@ -192,12 +202,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     if (tid == C::THREADS - 1) prefix[C::THREADS] = at + sum;
     __syncthreads();
   }
-  const int64_t total = prefix[C::THREADS];
-  const int64_t workers = static_cast<int64_t>(gridDim.x) * C::GROUPS;
-  const int64_t me = static_cast<int64_t>(blockIdx.x) * C::GROUPS + gq;
+  int64_t total = prefix[C::THREADS];
+  const int workers = gridDim.x * C::GROUPS, me = blockIdx.x * C::GROUPS + gq;
   int64_t at = me * total / workers;
-  const int64_t stop = (me + 1) * total / workers;
-  const int64_t begin = at;
+  int64_t stop = static_cast<int64_t>(me + 1) * total / workers;
+  int64_t begin = at;
   const uint32_t tab = table | (lane * 4);
   auto ring_of = [&](int w) { return w < C::FRONT ? smem + w * C::RING : tail + (w - C::FRONT) * C::RING; };
   uint8_t *ring = ring_of(warp);
@@ -215,6 +224,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
   constexpr int CC = C::CONSTS / 16;         // chunks of a part's key constants
   const int copy_dst = (lane / CH) * (D / 2) + (((lane % CH) ^ (swizzle<NB>(lane / CH) << 1)) << 4);
   const uint16_t *const_src = (lane < CC ? a.k_absmax : a.v_absmax) + (lane % (2 * NB)) * 8;
+  const bool one_tile_pages = a.kb.page_shift < 5;  // pages of 16: a part's two tiles lie apart
   const bool const_second = T == 2 && (lane % CC) >= CC / 2;  // of the part's second tile
   const uint32_t ring_addr = smem_u32(ring);
   if (gw == 0 && lane < 2) {  // no part yet
@@ -243,11 +253,32 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     }
     const int64_t rel = at - seq_start;
     const int item = static_cast<int>(rel / sp.steps);
-    const int step0 = static_cast<int>(rel - static_cast<int64_t>(item) * sp.steps);
-    const int head = item % a.heads, tile = item / a.heads;
-    const int64_t first = seq_start + static_cast<int64_t>(item) * sp.steps, end = first + sp.steps;
-    const int step1 = stop < end ? static_cast<int>(stop - first) : sp.steps;
-    const int row_limit = sp.q.n * a.group - tile * ROWS;  // rows of the tile that exist
+    int step0 = static_cast<int>(rel - static_cast<int64_t>(item) * sp.steps);
+    int head = item % a.heads, tile = item / a.heads;
+    int64_t first = seq_start + static_cast<int64_t>(item) * sp.steps, end = first + sp.steps;
+    int step1 = stop < end ? static_cast<int>(stop - first) : sp.steps;
+    if (lane == 0) {
+      state->at = at;
+      state->stop = stop;
+      state->begin = begin;
+      state->total = total;
+      state->seq_start = seq_start;
+      state->first = first;
+      state->end = end;
+      state->b = b;
+      state->head = head;
+      state->tile = tile;
+      state->step0 = step0;
+      state->step1 = step1;
+      state->row0 = sp.q.row0;
+      state->n = sp.q.n;
+      state->len = sp.q.len;
+      state->tiles = sp.tiles;
+      state->steps = sp.steps;
+      state->lo = sp.lo;
+    }
+    __syncwarp();
+    int row_limit = sp.q.n * a.group - tile * ROWS;  // rows of the tile that exist
 
     // ------------------------------------------------------------ query rows -> B operand
     uint32_t q[NT][NB][4][2];
@@ -346,37 +377,43 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     const int32_t *pages = a.kb.page_table + static_cast<int64_t>(b) * a.kb.max_pages;
     bool bad_page = false;
     auto load_pages = [&](int u, int (&page)[T]) {
+      const int tok = base_of(u);
+      page[0] = __ldg(pages + min(tok >> a.kb.page_shift, a.kb.max_pages - 1));
+      if (T == 2 && one_tile_pages) page[T - 1] = __ldg(pages + min((tok + 16) >> a.kb.page_shift, a.kb.max_pages - 1));
+    };
+    // cache row of the token `tok` on `page`; row 0 for tiles without a page
+    auto row_of = [&](int tok, int page) -> uint32_t {
+      const bool bad = static_cast<unsigned>(page) >= static_cast<unsigned>(a.kb.num_pages);
+      bad_page |= bad && tok < sp.q.len;
+      const uint32_t row = ((static_cast<uint32_t>(page) * a.heads + head) << a.kb.page_shift) +
+                           (tok & ((1 << a.kb.page_shift) - 1));
+      return bad ? 0 : row;
+    };
+    auto copy_codes = [&](uint32_t dst, const uint8_t *ks, const uint8_t *vs, int bytes) {
 #pragma unroll
-      for (int i = 0; i < T; ++i)
-        page[i] = __ldg(pages + min((base_of(u) + 16 * i) >> a.kb.page_shift, a.kb.max_pages - 1));
+      for (int j = 0; j < C::CODES; j += 512)  // 512 bytes each
+        if (j < bytes) {
+          copy16(dst + j, ks + j);
+          copy16(dst + C::CODES + j, vs + j);
+        }
     };
     auto copy_part = [&](int u, const int (&page)[T]) {
-      uint32_t row[T];  // cache row of each tile's first token; row 0 for tiles without a page
-#pragma unroll
-      for (int i = 0; i < T; ++i) {
-        const int tok = base_of(u) + 16 * i;
-        const bool bad = static_cast<unsigned>(page[i]) >= static_cast<unsigned>(a.kb.num_pages);
-        bad_page |= bad && tok < sp.q.len;
-        row[i] = bad ? 0
-                     : ((static_cast<uint32_t>(page[i]) * a.heads + head) << a.kb.page_shift) +
-                           (tok & ((1 << a.kb.page_shift) - 1));
-      }
       const uint32_t dst = ring_addr + (u % S) * C::PART_BYTES;
-#pragma unroll
-      for (int i = 0; i < T; ++i) {
-        const uint8_t *ks = a.k_codes + static_cast<uint64_t>(row[i]) * (D / 2) + lane * 16;
-        const uint8_t *vs = a.v_codes + static_cast<uint64_t>(row[i]) * (D / 2) + lane * 16;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {  // 512 bytes each
-          if (j * 512 + 512 <= 8 * D) {
-            copy16(dst + i * 8 * D + j * 512 + copy_dst, ks + j * 512);
-            copy16(dst + C::CODES + i * 8 * D + j * 512 + copy_dst, vs + j * 512);
-          }
-        }
+      const int tok = base_of(u);
+      const uint32_t row = row_of(tok, page[0]);
+      const uint64_t at = static_cast<uint64_t>(row) * (D / 2) + lane * 16;
+      uint32_t const_row = row;
+      if (T == 1 || !one_tile_pages) {  // the part's rows lie side by side
+        copy_codes(dst + copy_dst, a.k_codes + at, a.v_codes + at, C::CODES);
+        if (T == 2 && const_second) const_row += 16;
+      } else {
+        const uint32_t row1 = row_of(tok + 16, page[T - 1]);
+        const uint64_t at1 = static_cast<uint64_t>(row1) * (D / 2) + lane * 16;
+        copy_codes(dst + copy_dst, a.k_codes + at, a.v_codes + at, 8 * D);
+        copy_codes(dst + copy_dst + 8 * D, a.k_codes + at1, a.v_codes + at1, 8 * D);
+        if (const_second) const_row = row1;
       }
-      if (lane < 2 * CC)
-        copy16(dst + 2 * C::CODES + lane * 16,
-               const_src + static_cast<uint64_t>(const_second ? row[T - 1] : row[0]) * NB);
+      if (lane < 2 * CC) copy16(dst + 2 * C::CODES + lane * 16, const_src + static_cast<uint64_t>(const_row) * NB);
     };
     int page[T];
     {
@@ -597,6 +634,25 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     }
     copies_wait<0>();
     if (bad_page) kv_error(a.kb);
+    at = state->at;
+    stop = state->stop;
+    begin = state->begin;
+    total = state->total;
+    seq_start = state->seq_start;
+    first = state->first;
+    end = state->end;
+    b = state->b;
+    head = state->head;
+    tile = state->tile;
+    step0 = state->step0;
+    step1 = state->step1;
+    sp.q.row0 = state->row0;
+    sp.q.n = state->n;
+    sp.q.len = state->len;
+    sp.tiles = state->tiles;
+    sp.steps = state->steps;
+    sp.lo = state->lo;
+    row_limit = sp.q.n * a.group - tile * ROWS;
 
     // ------------------------------------------------------------ join the group's warps
 #pragma unroll
@@ -626,7 +682,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     const float *my_lse = lse + gq * 4 * ROWS;
     const bool whole = step0 == 0 && step1 == sp.steps;
     const int slot = at == begin ? 0 : 1;
-    const int64_t part = me * 2 + slot;
+    const int64_t part = static_cast<int64_t>(me) * 2 + slot;
     const int tl = tid & 127;
     for (int x = tl; x < ROWS * (D / 8); x += 128) {
       const int r = x / (D / 8), ch = (x % (D / 8)) * 8;
@@ -759,11 +815,21 @@ cudaError_t launch_kv_attention(const qlora_kv_cache &c, const KvBatch &kb, cons
   a.v_absmax = c.v_absmax;
   a.heads = c.heads;
   a.group = q_heads / c.heads;
-  // the grids whose levels are multiples of one value are stored as the (exact) multiples
-  const float unit = c.codebook == QLORA_CB_INT4 ? 7.0f : c.codebook == QLORA_CB_FP4_E2M1 ? 6.0f : 1.0f;
+  // Levels are held in fp16 times a unit.  The integer grid and E2M1 are (halves of) small
+  // integers at their unit, and exact; so is E3M0.  NF4's levels are rounded, within 2^-11 at any
+  // unit; what counts over a long cache, where random errors average out, is the sum of the
+  // rounding errors weighted by how often each level is met.  Of two million units in [1, 2) this
+  // one leaves the smallest: 2e-6 of the values' root mean square or less for values that are
+  // Gaussian, Laplace, uniform, Student's t or have strong channels (unit 1: up to 5e-5, which over
+  // 131071 tokens of random signs was an error of 0.003 of the output).
+  const float unit = c.codebook == QLORA_CB_NF4        ? 1.458608f
+                     : c.codebook == QLORA_CB_INT4     ? 7.0f
+                     : c.codebook == QLORA_CB_FP4_E2M1 ? 6.0f
+                                                       : 1.0f;
   for (int i = 0; i < 16; ++i) {
     float v = levels[i] * unit;
-    if (unit != 1.0f) v = static_cast<float>(static_cast<int>(v * 2.0f + (v < 0 ? -0.5f : 0.5f))) * 0.5f;
+    if (c.codebook == QLORA_CB_INT4 || c.codebook == QLORA_CB_FP4_E2M1)
+      v = static_cast<float>(static_cast<int>(v * 2.0f + (v < 0 ? -0.5f : 0.5f))) * 0.5f;
     a.levels[i] = __float2half_rn(v);
   }
   a.scale_log2 = scale * 1.4426950408889634f / unit;

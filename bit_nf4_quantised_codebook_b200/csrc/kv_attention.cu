@@ -51,6 +51,9 @@ namespace qlora {
 namespace {
 
 constexpr int kStepTokens = 128;     // tokens of one step of a group (4 warps x 32)
+// What starting and ending an item costs a group, in steps: its place on the line is that much
+// longer than its steps, so that a group with many short items gets fewer of them.
+constexpr int kItemOverhead = 3;
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -96,7 +99,9 @@ struct KvSpan {
   int tiles;   // row tiles per key/value head (0: no rows)
   int steps;   // steps of each item (at least 1 where there are rows)
   int lo;      // first cached token that a row may see, rounded down to 32
-  __device__ __forceinline__ int64_t units(int heads) const { return static_cast<int64_t>(tiles) * heads * steps; }
+  __device__ __forceinline__ int64_t units(int heads) const {
+    return static_cast<int64_t>(tiles) * heads * (steps + kItemOverhead);
+  }
 };
 __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs &a, int b, int tile_rows) {
   KvSpan s;
@@ -252,11 +257,16 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
       sp = kv_span(a, ++b, ROWS);
     }
     const int64_t rel = at - seq_start;
-    const int item = static_cast<int>(rel / sp.steps);
-    int step0 = static_cast<int>(rel - static_cast<int64_t>(item) * sp.steps);
+    const int units = sp.steps + kItemOverhead;  // the item's place on the line: its overhead, then its steps
+    const int item = static_cast<int>(rel / units);
     int head = item % a.heads, tile = item / a.heads;
-    int64_t first = seq_start + static_cast<int64_t>(item) * sp.steps, end = first + sp.steps;
-    int step1 = stop < end ? static_cast<int>(stop - first) : sp.steps;
+    int64_t first = seq_start + static_cast<int64_t>(item) * units, end = first + units;
+    int step0 = max(0, static_cast<int>(at - first) - kItemOverhead);
+    int step1 = (stop < end ? static_cast<int>(stop - first) : units) - kItemOverhead;
+    if (step1 <= step0) {  // this range ends before the item's first step
+      at = stop;
+      break;
+    }
     if (lane == 0) {
       state->at = at;
       state->stop = stop;
@@ -369,7 +379,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     // 16 tokens, copied STAGES - 1 parts ahead into this warp's ring.  A tile lies inside one
     // page, so its 16 slots can be copied whether or not the sequence ends among them; what
     // lies past the end is masked like what a row does not see.
-    const int units = (step1 - step0) * C::PARTS;
+    const int parts = (step1 - step0) * C::PARTS;
     auto base_of = [&](int u) {
       return sp.lo + (step0 + u / C::PARTS) * kStepTokens + gw * 32 + (u % C::PARTS) * (T * 16);
     };
@@ -423,11 +433,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
       load_pages(S, page);
 #pragma unroll
       for (int j = 0; j < S; ++j) {
-        if (j < units) copy_part(j, first_pages[j]);
+        if (j < parts) copy_part(j, first_pages[j]);
         copies_commit();
       }
     }
-    for (int u = 0; u < units; ++u) {
+    for (int u = 0; u < parts; ++u) {
       const int tok0 = base_of(u);
       copies_wait<S - 1>();
       __syncwarp();  // every lane's copies of this part are there
@@ -628,7 +638,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
         }
       }
       __syncwarp();  // every lane has read this part
-      if (u + S < units) copy_part(u + S, page);
+      if (u + S < parts) copy_part(u + S, page);
       copies_commit();
       load_pages(u + S + 1, page);
     }
@@ -731,14 +741,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
       p.b = b;
       p.head = head;
       p.tile = tile;
-      p.g0 = group_of(first);
+      p.g0 = group_of(first + kItemOverhead);  // holds the item's first step
       p.last = group_of(end - 1);
-      p.head_slot = p.g0 * total / workers == first ? 0 : 1;
-      p.joins = at != first && at == (p.g0 + 1) * total / workers ? 1 : 0;
+      p.head_slot = p.g0 * total / workers >= first ? 0 : 1;
+      p.joins = step0 > 0 && at == (p.g0 + 1) * total / workers ? 1 : 0;
       a.parts[part] = p;
     }
     named_barrier(1 + gq, 128);  // the rings are free again
-    at = first + step1;
+    at = first + kItemOverhead + step1;
   }
 }
 

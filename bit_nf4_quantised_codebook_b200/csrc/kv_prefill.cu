@@ -71,6 +71,8 @@ struct PreCfg {
 // into the fp16 operands: keys keep all their bits (fp16 has 25 binades below 2^12), and a
 // weight that vanishes in fp16 (2^-31 of the largest) can have a value 2^8 times another's.
 constexpr int kNearKeys = 12, kNearValues = 8;
+// What starting and ending an item costs a CTA, in steps: part of its place on the line.
+constexpr int kItemOverhead = 2;
 constexpr unsigned long long kDrainNs = 1000000000ull;  // bound on the wait for the MMAs in flight at the end
 
 // How a step's keys and values were written (by the decoding warps, for the others).  Where
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const __grid_constant_
       t.lo = a.window > 0 ? max(0, min(q.len, q.pos0() + i0 - a.window + 1)) & ~31 : 0;
       t.steps = max(1, (see - t.lo + C::N - 1) / C::N);
       p.entries[e] = t;
-      units = static_cast<int64_t>(t.steps) * a.heads;
+      units = static_cast<int64_t>(t.steps + kItemOverhead) * a.heads;
     }
     const int64_t upto = scan(units);
     if (e < count) p.prefix[e] = carry + upto - units;
@@ -193,7 +195,8 @@ struct Segment {
   int rows;          // rows of the tile that exist (at most ROWS: the second half stays idle with one row tile)
   bool whole;        // the item is this worker's alone
   int slot;
-  int64_t first, end, at;  // the item's steps on the line, and where this part begins
+  int used;          // of the line
+  int64_t first, end, at;  // the item's place on the line, and where this part begins
 };
 
 // This worker's parts, in order.  A role keeps two integers between its parts, and reads
@@ -201,7 +204,7 @@ struct Segment {
 // spilled, and with all of shared memory in use a spilled value is a second-level cache
 // access away.
 template <class C>
-__device__ __forceinline__ bool next_part(const PrefillArgs &p, int &e, int done, Segment &s) {
+__device__ __forceinline__ bool next_part(const PrefillArgs &p, int &e, int done, Segment &s) {  // done: of the line
   const int64_t total = p.prefix[*p.count], workers = gridDim.x, me = blockIdx.x;
   const int64_t begin = me * total / workers, stop = (me + 1) * total / workers, at = begin + done;
   if (at >= stop) return false;
@@ -211,11 +214,14 @@ __device__ __forceinline__ bool next_part(const PrefillArgs &p, int &e, int done
   s.b = t.b;
   s.tile = t.tile;
   s.lo = t.lo;
-  s.head = static_cast<int>(rel / t.steps);
-  s.step0 = static_cast<int>(rel - static_cast<int64_t>(s.head) * t.steps);
-  s.first = base + static_cast<int64_t>(s.head) * t.steps;
-  s.end = s.first + t.steps;
-  s.step1 = stop < s.end ? static_cast<int>(stop - s.first) : t.steps;
+  const int units = t.steps + kItemOverhead;
+  s.head = static_cast<int>(rel / units);
+  s.first = base + static_cast<int64_t>(s.head) * units;
+  s.end = s.first + units;
+  s.step0 = max(0, static_cast<int>(at - s.first) - kItemOverhead);
+  s.step1 = (stop < s.end ? static_cast<int>(stop - s.first) : units) - kItemOverhead;
+  if (s.step1 <= s.step0) return false;  // the range ends before the item's first step
+  s.used = static_cast<int>(s.first + kItemOverhead + s.step1 - at);
   s.whole = s.step0 == 0 && s.step1 == t.steps;
   s.slot = at == begin ? 0 : 1;
   s.at = at;
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       nsteps = sg.step1 - sg.step0;
       if (m * 128 >= sg.rows) {  // no row in this half
         all_steps += nsteps;
-        done_steps += nsteps;
+        done_steps += sg.used;
         continue;
       }
       // ---- the query row: scaled to fp16, into the swizzled operand
@@ -581,7 +587,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       tc_fence_after();
       Segment sg;
       next_part<C>(p, entry, done_steps, sg);
-      done_steps += nsteps;
+      done_steps += sg.used;
       const int row = m * 128 + r, rr = sg.tile * C::ROWS + row;
       const bool live = row < sg.rows;
       const int tok = live ? rr / a.group : 0, h = live ? rr - tok * a.group : 0;
@@ -626,10 +632,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           kp.b = sg.b;
           kp.head = sg.head;
           kp.tile = sg.tile;
-          kp.g0 = worker_of(sg.first);
+          kp.g0 = worker_of(sg.first + kItemOverhead);  // holds the item's first step
           kp.last = worker_of(sg.end - 1);
-          kp.head_slot = kp.g0 * total / workers == sg.first ? 0 : 1;
-          kp.joins = sg.at != sg.first && sg.at == (kp.g0 + 1) * total / workers ? 1 : 0;
+          kp.head_slot = kp.g0 * total / workers >= sg.first ? 0 : 1;
+          kp.joins = sg.step0 > 0 && sg.at == (kp.g0 + 1) * total / workers ? 1 : 0;
           a.parts[part] = kp;
         }
       }
@@ -670,7 +676,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         head = sg.head;
         len = sg.q.len;
         pages = a.kb.page_table + static_cast<int64_t>(sg.b) * a.kb.max_pages;
-        done_steps += nsteps;
+        done_steps += sg.used;
       }
       bool bad_page = false;
       auto tile_of = [&](int i) { return dw + i * warps; };
@@ -894,7 +900,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         if (!next_part<C>(p, entry, done_steps, sg)) break;
         tiles = MT == 2 && sg.rows > 128 ? 2 : 1;
         nsteps = sg.step1 - sg.step0;
-        done_steps += nsteps;
+        done_steps += sg.used;
       }
       for (int m = 0; m < tiles && ok; ++m) ok = wait_all(&qfull[m], queries[m]++ & 1);
       if (ok) ok = wait_all(kfull, n & 1);

@@ -57,11 +57,11 @@ struct PreCfg {
   static constexpr int TMEM_COLS = 512;
   static constexpr int THREADS = 16 * 32;
   // registers of a thread: softmax and the others; together what the CTA starts with
-  static constexpr int REGS_SOFTMAX = 144, REGS_OTHERS = 112;
+  static constexpr int REGS_SOFTMAX = 136, REGS_OTHERS = 120;
   static_assert(256 * REGS_SOFTMAX + 256 * REGS_OTHERS == 128 * THREADS, "register split");
   static constexpr int BARS = 19;
   static constexpr int MISC_FLOATS = 2 * N + 2 * NB * N;
-  static constexpr int MISC_BYTES = MISC_FLOATS * 4 + 4 * 8 + 2 * 7 * 8 + BARS * 8 + 32;
+  static constexpr int MISC_BYTES = MISC_FLOATS * 4 + 4 * 8 + 2 * 7 * 8 + BARS * 8 + 48;
   static constexpr int SMEM_BYTES = 0x20000 + KV_BYTES + MT * Q_BYTES;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
   static_assert(O_COL + MT * D <= TMEM_COLS, "TMEM columns");
@@ -204,13 +204,18 @@ struct Segment {
 // spilled, and with all of shared memory in use a spilled value is a second-level cache
 // access away.
 template <class C>
-__device__ __forceinline__ bool next_part(const PrefillArgs &p, int &e, int done, Segment &s) {  // done: of the line
-  const int64_t total = p.prefix[*p.count], workers = gridDim.x, me = blockIdx.x;
-  const int64_t begin = me * total / workers, stop = (me + 1) * total / workers, at = begin + done;
+__device__ __forceinline__ bool next_part(const PrefillArgs &p, const volatile int64_t *my_line, int &e, int done, Segment &s) {
+  const int64_t begin = my_line[0], stop = my_line[1], at = begin + done;  // done: of the line
   if (at >= stop) return false;
-  while (at >= p.prefix[e + 1]) ++e;
-  const KvEntry t = p.entries[e];
-  const int64_t base = p.prefix[e], rel = at - base;
+  KvEntry t = p.entries[e];
+  int64_t base = p.prefix[e], after = p.prefix[e + 1];
+  while (at >= after) {
+    ++e;
+    t = p.entries[e];
+    base = after;
+    after = p.prefix[e + 1];
+  }
+  const int64_t rel = at - base;
   s.b = t.b;
   s.tile = t.tile;
   s.lo = t.lo;
@@ -312,6 +317,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + C::BARS);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   int *s_entry = reinterpret_cast<int *>(tmem_slot + 2);
+  volatile int64_t *my_line = reinterpret_cast<int64_t *>(tmem_slot + 4);  // this worker's steps on the line
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (table - smem_base < C::KV_BYTES + 1024 + C::MISC_BYTES) {  // cannot happen while shared memory starts low
@@ -362,7 +368,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       hi = min(hi, nlo + stride);
       lo = nlo;
     }
-    if (lane == 0) *s_entry = lo;
+    if (lane == 0) {
+      *s_entry = lo;
+      my_line[0] = at;
+      my_line[1] = static_cast<int64_t>(blockIdx.x + 1) * p.prefix[count] / gridDim.x;
+    }
   }
   if (tid == 0)
     for (int i = 0; i < 2; ++i) {
@@ -393,7 +403,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       float qs = 0.0f;
       {
       Segment sg;
-      if (!next_part<C>(p, entry, done_steps, sg)) break;
+      if (!next_part<C>(p, my_line, entry, done_steps, sg)) break;
       nsteps = sg.step1 - sg.step0;
       if (m * 128 >= sg.rows) {  // no row in this half
         all_steps += nsteps;
@@ -408,14 +418,22 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       {
         const uint16_t *src = a.Q + static_cast<int64_t>(sg.q.row0 + tok) * a.q_token_stride +
                               static_cast<int64_t>(sg.head * a.group + h) * a.q_head_stride;
+        constexpr bool ONCE = D <= 128;  // the row fits the registers between its two uses
+        uint4 raw[ONCE ? D / 8 : 1];
         uint32_t mag = 0;
-        if (live) {
+        auto look = [&](const uint4 &u) {
+          mag = __vmaxu2(__vmaxu2(mag, u.x & 0x7FFF7FFFu), u.y & 0x7FFF7FFFu);
+          mag = __vmaxu2(__vmaxu2(mag, u.z & 0x7FFF7FFFu), u.w & 0x7FFF7FFFu);
+        };
+        if constexpr (ONCE) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c)
+            raw[c] = live ? __ldg(reinterpret_cast<const uint4 *>(src) + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) look(raw[c]);
+        } else if (live) {
 #pragma unroll 8
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-            mag = __vmaxu2(__vmaxu2(mag, u.x & 0x7FFF7FFFu), u.y & 0x7FFF7FFFu);
-            mag = __vmaxu2(__vmaxu2(mag, u.z & 0x7FFF7FFFu), u.w & 0x7FFF7FFFu);
-          }
+          for (int c = 0; c < D / 8; ++c) look(__ldg(reinterpret_cast<const uint4 *>(src) + c));
         }
         mag = max(mag >> 16, mag & 0xFFFFu);
         int e = static_cast<int>(mag >> 7) - 127 - 13;  // largest magnitude in [2^13, 2^14)
@@ -423,16 +441,21 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         e = max(e, -120);
         const float down = pow2(-e);
         const uint32_t dst = q_smem + m * C::Q_BYTES + r * 128;
-#pragma unroll 8
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (live) u = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+        auto write = [&](int c, const uint4 &u) {
           const uint32_t in[4] = {u.x, u.y, u.z, u.w};
           uint32_t o[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             o[i] = pack_half2(__uint_as_float(in[i] << 16) * down, __uint_as_float(in[i] & 0xFFFF0000u) * down);
           st_shared_v4(dst + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+        };
+        if constexpr (ONCE) {
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) write(c, raw[c]);
+        } else {
+#pragma unroll 8
+          for (int c = 0; c < D / 8; ++c)
+            write(c, live ? __ldg(reinterpret_cast<const uint4 *>(src) + c) : make_uint4(0, 0, 0, 0));
         }
         qs = pow2(e) * a.scale_log2;
         if (mag >= 0x7F80u) qs = __uint_as_float(0x7FC00000u);  // a non-finite query: its row is NaN throughout
@@ -586,7 +609,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       }
       tc_fence_after();
       Segment sg;
-      next_part<C>(p, entry, done_steps, sg);
+      next_part<C>(p, my_line, entry, done_steps, sg);
       done_steps += sg.used;
       const int row = m * 128 + r, rr = sg.tile * C::ROWS + row;
       const bool live = row < sg.rows;
@@ -670,7 +693,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       const int32_t *pages;
       {
         Segment sg;
-        if (!next_part<C>(p, entry, done_steps, sg)) break;
+        if (!next_part<C>(p, my_line, entry, done_steps, sg)) break;
         nsteps = sg.step1 - sg.step0;
         lo = sg.lo + sg.step0 * N;
         head = sg.head;
@@ -897,7 +920,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       int tiles, nsteps;
       {
         Segment sg;
-        if (!next_part<C>(p, entry, done_steps, sg)) break;
+        if (!next_part<C>(p, my_line, entry, done_steps, sg)) break;
         tiles = MT == 2 && sg.rows > 128 ? 2 : 1;
         nsteps = sg.step1 - sg.step0;
         done_steps += sg.used;

@@ -10,9 +10,8 @@
 // permute that picks the byte out of a code word builds the lookup's address in the
 // same instruction (entry stride 256 bytes, table at a multiple of 64 KiB) and 32 lanes
 // never share a bank.  The products run on mma.sync m16n8k16: with a handful of query
-// rows per key/value head the tensor pipe is not what bounds this kernel, and the
-// register layouts of its operands let the codes go from global memory to registers
-// with no staging:
+// rows per key/value head the tensor pipe is not what bounds this kernel (22 % busy), and
+// its operands' register layouts let decoded pairs be used as they come:
 //   S^T (16 tokens x 8 rows) = K (A operand: token rows, codes decoded in place) * Q^T
 //   O^T (16 channels x 8 rows) += V^T (A operand: pairs of tokens of one channel per
 //        register, formed by merging the nibbles of two tokens' words) * P^T
@@ -37,6 +36,13 @@
 // tokens with its own running statistics; a group joins its four warps through shared
 // memory at the end of its part of an item.  An item that several groups shared is joined
 // from their normalised parts, in order, by a second small kernel.
+//
+// Bound by the issue of the decoding: 2.9 instructions per element (one of them the lookup
+// and permute of a pair's half, a quarter the copies and the softmax), load/store pipe 68 %
+// and integer pipe 49 % busy.  64 sequences of 1 to 8192 tokens, 64 query and 8 key/value
+// heads of 128: 87 us, 3.45 TB/s of codes and constants (0.54 of the measured copy rate); one
+// sequence of 131071: 49 us.  Codes loaded straight into registers took 62 us for the latter
+// (one 32-byte sector per request), registers spilled beside a full shared memory 4 us.
 #include <atomic>
 #include <climits>
 #include <cstdint>
@@ -53,7 +59,7 @@ namespace {
 constexpr int kStepTokens = 128;     // tokens of one step of a group (4 warps x 32)
 // What starting and ending an item costs a group, in steps: its place on the line is that much
 // longer than its steps, so that a group with many short items gets fewer of them.
-constexpr int kItemOverhead = 3;
+constexpr int kItemOverhead = 3;  // 64 uneven sequences: 112 us without, 98, 87, 87, 89 us with 1, 2, 3, 5
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"

@@ -7,27 +7,36 @@
 // one CTA per SM; parts of items that CTAs share are joined by k_kv_join.
 //
 // A CTA's roles:
-//   warps 0-3, 4-7  softmax of 128 rows each, one row per thread, ping-pong: while one half
-//                   works on its scores the tensor cores serve the other
-//   warps 8-11      decode the step's keys and values from codes to fp16 in the 128-byte
-//                   swizzled operand layout: once for all 256 rows
-//   warp 12         one thread issues the MMAs
+//   warps 0-3, 4-7  softmax of 128 rows each, one row per thread: while one half works on its
+//                   scores the tensor cores serve the other
+//   warps 8-11      decode the step's keys from codes to fp16 in the 128-byte swizzled operand
+//                   layout, once for all 256 rows
+//   warp 12         issues the MMAs
+//   warps 13-15     decode the step's values
 // S = Q K^T (Q and K in shared memory) lands in TMEM; the softmax warps read it, replace it
-// in place by the weights P_b in fp16, one set per block of 64 channels, and P_b is the A
-// operand, from TMEM, of O_b += P_b V_b.  The values' constants multiply the weights, so
-// decoding a value is a table lookup and nothing else; the keys' constants multiply the
-// levels as fp16 numbers with at most 8 significant bits (times a power of two per token
-// that goes into the scores).
+// in place by fp16 weights, and those are the A operand, from TMEM, of O += P V.
 //
-// Numbers: as in kv_attention.cu (levels and weights in fp16, everything else float32),
-// and one more rounding of level x constant to fp16 for the keys (2^-11).  Per row, weights
-// are 2^(s - r) * cV with one reference r for all blocks, renewed when some weight passes
-// about 2^14 (then the largest contribution so far weighs 2^6 or more), so a block whose constants
-// are below 2^-20 of another block's loses bits.  Constants are taken relative to the
-// largest exponent among 32 tokens, so no range of constants overflows float32.
+// The blocks' constants.  Where the constants of a step lie within a few binades of one
+// another (every step of ordinary data) they are multiplied into the fp16 levels, relative to
+// one exponent for the step's keys and one for its values.  Where they do not - a constant far
+// from the others, or not finite - the step is "wide": each token's keys have an exponent of
+// their own that multiplies its scores, the values stay levels, and their constants multiply
+// the weights, one set of weights and one product per block of 64 channels.  So a value that a
+// row does not see can be of any size, or NaN, and leaves the row as it is.
 //
-// Bound by: the shared-memory traffic of the MMAs' operands (A and B of Q K^T and B of P V
-// are read at 128 bytes per clock) and the issue slots of the softmax, about equally.
+// Numbers.  As in kv_attention.cu: levels and weights in fp16 (2^-11 each), everything else
+// float32; and one more rounding of level x constant to fp16 (2^-11) for NF4.  A row's
+// weights are 2^(s - r), r renewed when one passes 2^14: the largest then weighs 2^6, and what
+// is 2^-31 of it vanishes (its value can be 2^8 times another's of the step: 2^-23).
+//
+// Measured (4096 tokens x 4 query heads over 8192 cached, 8 key/value heads of 128): 0.59 ms,
+// 696 TFLOP/s of the visible pairs.  A step takes 5600 clocks, of which the tensor cores work
+// 2100: it is bound by the chain from one step of a row tile to the next (softmax 3150 clocks,
+// the two products and their hand-overs 1800) and by the decoding of the values between two
+// products that use them (2400).  Tried without gain: values in two stages (more decoding next
+// to the softmax slows it as much), scores in two halves (products of 64 columns), 20 warps,
+// two passes of the softmax between checks (spills, and with shared memory full a spilled
+// register is a second-level cache access).
 #include <atomic>
 #include <cstdint>
 #include <cuda_fp16.h>

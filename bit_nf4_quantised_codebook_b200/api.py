@@ -446,10 +446,10 @@ def _kv_stream(device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class KVCache:
     """A paged cache of keys and values in 4 bits (qlora_kv_cache of the C header).
-    The buffers are kept in place for the cache's lifetime."""
+    Its buffers stay the same for its lifetime; their contents may be rewritten."""
     num_pages: int
     page_size: int
     heads: int                 # key/value heads
@@ -472,10 +472,11 @@ class KVCache:
             _need(absmax, torch.bfloat16, rows + (self.head_dim // 64,), side + "_absmax")
             if codes.device != self.k_codes.device or absmax.device != self.k_codes.device:
                 raise QloraError("KVCache: the buffers are on different devices")
-        self._c = _KVCache(self.num_pages, self.page_size, self.heads, self.head_dim, CODEBOOKS[self.codebook],
-                           self.k_codes.data_ptr(), self.k_absmax.data_ptr(), self.v_codes.data_ptr(),
-                           self.v_absmax.data_ptr())
-        self._device = self.k_codes.get_device()
+        c = _KVCache(self.num_pages, self.page_size, self.heads, self.head_dim, CODEBOOKS[self.codebook],
+                     self.k_codes.data_ptr(), self.k_absmax.data_ptr(), self.v_codes.data_ptr(),
+                     self.v_absmax.data_ptr())
+        object.__setattr__(self, "_c", c)
+        object.__setattr__(self, "_device", self.k_codes.get_device())
 
     def nbytes(self) -> int:
         return 2 * (self.k_codes.numel() + 2 * self.k_absmax.numel())
@@ -492,10 +493,10 @@ def alloc_kv_cache(num_pages: int, heads: int, head_dim: int, page_size: int = 6
                    new(head_dim // 64, torch.bfloat16))
 
 
-@dataclass
+@dataclass(frozen=True, eq=False)
 class KVBatch:
     """The sequences of one call (qlora_kv_batch of the C header), int32 on the device.
-    The arrays may be rewritten in place between calls."""
+    The arrays stay the same; their contents may be rewritten between calls."""
     token_start: torch.Tensor  # [batch + 1]: sequence b owns token rows token_start[b] .. token_start[b + 1] - 1
     kv_len: torch.Tensor       # [batch]: cached tokens, the call's own included
     page_table: torch.Tensor   # [batch, max_pages]
@@ -509,16 +510,17 @@ class KVBatch:
         _need(self.page_table, torch.int32, (batch, max_pages), "page_table")
         if len({t.device for t in (self.token_start, self.kv_len, self.page_table)}) != 1:
             raise QloraError("KVBatch: the arrays are on different devices")
-        self.batch, self.max_pages = batch, max_pages
-        self._device = self.kv_len.get_device()
-        self._last = (-1, None)  # tokens and the descriptor made for them
+        object.__setattr__(self, "batch", batch)
+        object.__setattr__(self, "max_pages", max_pages)
+        object.__setattr__(self, "_device", self.kv_len.get_device())
+        object.__setattr__(self, "_last", (-1, None))  # tokens and the descriptor made for them
 
     def c_struct(self, tokens: int) -> _KVBatch:
         known, c = self._last
         if known != tokens:
             c = _KVBatch(self.batch, self.max_pages, tokens, self.token_start.data_ptr(), self.kv_len.data_ptr(),
                          self.page_table.data_ptr())
-            self._last = (tokens, c)
+            object.__setattr__(self, "_last", (tokens, c))
         return c
 
 

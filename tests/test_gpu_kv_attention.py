@@ -64,14 +64,33 @@ def test_several_tokens_and_masks(dim, causal, window, heads, group):
 @pytest.mark.parametrize("dim,heads,group", [(128, 2, 4), (64, 4, 1), (256, 1, 8), (128, 1, 7)])
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 200)])
 def test_prompt_chunks(dim, heads, group, causal, window):
-    """Hundreds of rows per sequence, beside single tokens in the same call."""
-    case = Case([257, 1, 130, 64, 1], [600, 333, 130, 1000, 2], page_size=64, pad=3, seed=3)
+    """Hundreds of rows per sequence, beside single tokens in the same call; more rows than cached
+    tokens, and none cached."""
+    case = Case([257, 1, 130, 64, 1, 100, 90], [600, 333, 130, 1000, 2, 40, 0], page_size=64, pad=3, seed=3)
     _run(case, heads, group, dim, causal=causal, window=window)
 
 
 def test_one_long_sequence():
     """Every group of warps of the GPU shares each item; the parts are joined."""
     _run(Case([1], [20_011], page_size=128, seed=4), 2, 8, 128)
+
+
+def test_rounding_of_levels_cancels_over_a_long_cache():
+    """100000 tokens with nearly equal weights: the outputs are averages of values of random signs,
+    360 times smaller than they, and any common bias of the decoded values would show.  The error's
+    2-norm over the outputs': bfloat16 rounding at most 2^-8 / sqrt(3) in the mean square (half a step
+    is 2^-8, uniform); levels and weights 2^-11 / sqrt(3) each, independent from token to token; the
+    levels' mean error, 2.3e-6 of the values' root mean square, grows by sqrt(100000) against it: 7.3e-4
+    (the keys' move the weights together and cancel in the softmax)."""
+    a = api()
+    length, heads, group, dim = 100_000, 4, 4, 128
+    case = Case([1], [length], page_size=256, seed=20)
+    c, mirror = filled_cache(a, case, heads, dim, "nf4", np.random.default_rng(96))
+    Q = bf16(np.random.default_rng(97).standard_normal((1, heads * group, dim)) * 0.1).cuda()
+    out = a.qlora_kv_attention(c, case.batch(a), Q)
+    want, _ = kv.attention(f64(Q), *mirror[0], dim ** -0.5, True, 0, True)
+    off = np.linalg.norm(f64(out) - want) / np.linalg.norm(want)
+    assert off <= np.sqrt(2.0 ** -16 / 3 + 3 * 2.0 ** -22 / 3 + 7.3e-4 ** 2), off
 
 
 def test_long_prompt():
@@ -325,7 +344,7 @@ def test_pool_larger_than_4_gib():
     moved = case.batch(a)
     for name in ("k_codes", "k_absmax", "v_codes", "v_absmax"):
         getattr(c, name)[pages - case.num_pages:] = getattr(small, name)
-    moved.page_table += pages - case.num_pages
+    moved.page_table.add_(pages - case.num_pages)
     Q = bf16(rng.standard_normal((case.tokens, 32, dim))).cuda()
     err = a.new_error_word()
     out = a.qlora_kv_attention(c, moved, Q, dev_err=err)

@@ -805,6 +805,9 @@ constexpr int kFewRows = 64;
 // few-row kernel takes the whole call (right for any number of rows, each 16 of them decoding
 // the cache anew).  Measured: the many-row kernel's launches cost a call without use for them
 // 11 us (64 single tokens over 2800 on average, 8 rows each: 117 against 128 us).
+// Single tokens stay here for any number of query heads too: with 128 of them on one key/value
+// head, one sequence of 32768 tokens takes 32 us (many-row kernel: 71), 16 of 4096 48 us (45); only
+// 64 of 2048 would be better off there (81 against 59 us).
 constexpr int64_t kSpreadRows = 512;
 bool may_have_many_rows(int64_t tokens, int batch, int group) { return (tokens - batch) * group > kSpreadRows; }
 }  // namespace

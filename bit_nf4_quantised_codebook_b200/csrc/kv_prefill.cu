@@ -150,15 +150,17 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const __grid_constant_
     sum += tiles[i];
   }
   const int64_t incl = scan(sum);
-  int off = static_cast<int>(incl - sum);
+  // (sequences that share rows, an error, may list any number: held below what an int holds)
+  constexpr int64_t kMost = 1 << 30;
+  int off = static_cast<int>(min(incl - sum, kMost));
 #pragma unroll
   for (int i = 0; i < QLORA_KV_MAX_BATCH / kPlanThreads; ++i) {
     if (b0 + i < b1) s_off[b0 + i] = off;
     off += tiles[i];
   }
-  if (tid == kPlanThreads - 1) s_off[a.kb.batch] = static_cast<int>(incl);
+  if (tid == kPlanThreads - 1) s_off[a.kb.batch] = static_cast<int>(min(incl, kMost));
   __syncthreads();
-  // sequences that share rows (an error, reported where they are read) may list more than there is room for
+  // ... and more than there is room for
   const int count = min(s_off[a.kb.batch], p.max_entries);
   if (count < s_off[a.kb.batch] && tid == 0) kv_error(a.kb);
   int64_t carry = 0;
@@ -481,7 +483,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       float ref = kFloor, mx = kFloor, rv = kFloor, l = 0.0f;
       for (int step = 0; step < nsteps; ++step, ++steps_done, ++all_steps, tok0 += N) {
         const int st = all_steps & 1;
-        ok = wait(&cfull[st], (all_steps >> 1) & 1) && wait(&sfull[m], steps_done & 1);
+        // The scores first: while this half sat out items, phases of cfull passed that it did not wait
+        // for, and a parity alone does not tell them apart.  With this step's scores there, the phase
+        // of two steps ago is over (the products of its values were issued before them).
+        ok = wait(&sfull[m], steps_done & 1) && wait(&cfull[st], (all_steps >> 1) & 1);
         if (!__all_sync(0xFFFFFFFFu, ok)) {
           ok = false;
           break;

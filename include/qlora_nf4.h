@@ -401,7 +401,7 @@ typedef struct qlora_kv_cache {
  *                            kv_len[b] - n_b + i: the rows are its last n_b.
  *   page_table  [batch][max_pages]  position p is slot p % page_size of page
  *                            page_table[b][p / page_size]; entries past the
- *                            sequence's last page are not read.
+ *                            sequence's last page may hold anything.
  * `tokens` is the number of rows of the call's tensors; rows that no sequence
  * owns (padding behind the last one) are neither read nor written.
  * Values that only the device sees are checked there.  A token_start pair that
@@ -470,8 +470,8 @@ qlora_status qlora_kv_attention_workspace_size(const qlora_kv_cache *cache, int 
  * reads key/value head h / (q_heads / heads).  out: device bfloat16
  * [tokens][q_heads][head_dim], 16-byte aligned, not overlapping Q.  The new
  * tokens' own keys and values must have been appended before.  scale > 0.
- * Scores, softmax statistics and sums are float32; identical inputs give
- * identical bits.
+ * Scores, softmax statistics and sums are float32 (keys past 2^100 may overflow
+ * the scores, and their rows become NaN); identical inputs give identical bits.
  * A non-finite stored constant or query makes the rows (and, for a value, the
  * 64 channels) that see it NaN and no others.
  */

@@ -304,6 +304,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ void st_global_v8(float *p, const float *f) {  // 32-byte aligned
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
+               "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+               : "memory");
+}
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&w)[4]) { ld_shared_v4(addr, w[0], w[1], w[2], w[3]); }
 
@@ -427,47 +432,57 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       const int rr = sg.tile * C::ROWS + row;
       const int tok = live ? rr / a.group : 0, h = live ? rr - tok * a.group : 0;
       {
-        const uint16_t *src = a.Q + static_cast<int64_t>(sg.q.row0 + tok) * a.q_token_stride +
-                              static_cast<int64_t>(sg.head * a.group + h) * a.q_head_stride;
-        constexpr bool ONCE = D <= 128;  // the row fits the registers between its two uses
-        uint4 raw[ONCE ? D / 8 : 1];
+        // A warp reads its 32 rows four at a time, 128 bytes of each by eight lanes (a row per lane
+        // touches 32 lines with every load: 6000-10000 clocks against 4000-6000).
+        const int64_t from = static_cast<int64_t>(sg.q.row0 + tok) * a.q_token_stride +
+                             static_cast<int64_t>(sg.head * a.group + h) * a.q_head_stride;
+        const unsigned there = __ballot_sync(0xFFFFFFFFu, live);
+        constexpr int BATCH = NB == 4 ? 4 : 8;  // loads in flight: of this many rows
+        auto exponent_of = [](uint32_t mag) {     // largest magnitude in [2^13, 2^14)
+          const int x = mag == 0 || mag >= 0x7F80u ? 0 : static_cast<int>(mag >> 7) - 127 - 13;
+          return max(x, -120);
+        };
         uint32_t mag = 0;
-        auto look = [&](const uint4 &u) {
-          mag = __vmaxu2(__vmaxu2(mag, u.x & 0x7FFF7FFFu), u.y & 0x7FFF7FFFu);
-          mag = __vmaxu2(__vmaxu2(mag, u.z & 0x7FFF7FFFu), u.w & 0x7FFF7FFFu);
-        };
-        if constexpr (ONCE) {
+#pragma unroll 1
+        for (int g0 = 0; g0 < 8; g0 += BATCH) {
+          uint4 raw[BATCH][NB];
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c)
-            raw[c] = live ? __ldg(reinterpret_cast<const uint4 *>(src) + c) : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < BATCH; ++i) {
+            const int x = (g0 + i) * 4 + (lane >> 3);
+            const uint16_t *src = a.Q + __shfl_sync(0xFFFFFFFFu, from, x) + (lane & 7) * 8;
 #pragma unroll
-          for (int c = 0; c < D / 8; ++c) look(raw[c]);
-        } else if (live) {
-#pragma unroll 8
-          for (int c = 0; c < D / 8; ++c) look(__ldg(reinterpret_cast<const uint4 *>(src) + c));
+            for (int k = 0; k < NB; ++k)
+              raw[i][k] = there >> x & 1 ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * k)) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < BATCH; ++i) {
+            const int x = (g0 + i) * 4 + (lane >> 3);
+            uint32_t most = 0;
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+              most = __vmaxu2(__vmaxu2(most, raw[i][k].x & 0x7FFF7FFFu), raw[i][k].y & 0x7FFF7FFFu);
+              most = __vmaxu2(__vmaxu2(most, raw[i][k].z & 0x7FFF7FFFu), raw[i][k].w & 0x7FFF7FFFu);
+            }
+            most = max(most >> 16, most & 0xFFFFu);
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
+            most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 4));
+            const float down = pow2(-exponent_of(most));
+            const uint32_t dst = q_smem + m * C::Q_BYTES + ((warp & 3) * 32 + x) * 128 + (((lane & 7) ^ (x & 7)) << 4);
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+              const uint32_t in[4] = {raw[i][k].x, raw[i][k].y, raw[i][k].z, raw[i][k].w};
+              uint32_t o[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                o[y] = pack_half2(__uint_as_float(in[y] << 16) * down, __uint_as_float(in[y] & 0xFFFF0000u) * down);
+              st_shared_v4(dst + k * 16384, o[0], o[1], o[2], o[3]);
+            }
+            const uint32_t of_row = __shfl_sync(0xFFFFFFFFu, most, (lane & 3) * 8);  // of row 4 (g0 + i) + lane % 4
+            if (lane >> 2 == g0 + i) mag = of_row;
+          }
         }
-        mag = max(mag >> 16, mag & 0xFFFFu);
-        int e = static_cast<int>(mag >> 7) - 127 - 13;  // largest magnitude in [2^13, 2^14)
-        if (mag == 0 || mag >= 0x7F80u) e = 0;
-        e = max(e, -120);
-        const float down = pow2(-e);
-        const uint32_t dst = q_smem + m * C::Q_BYTES + r * 128;
-        auto write = [&](int c, const uint4 &u) {
-          const uint32_t in[4] = {u.x, u.y, u.z, u.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            o[i] = pack_half2(__uint_as_float(in[i] << 16) * down, __uint_as_float(in[i] & 0xFFFF0000u) * down);
-          st_shared_v4(dst + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-        };
-        if constexpr (ONCE) {
-#pragma unroll
-          for (int c = 0; c < D / 8; ++c) write(c, raw[c]);
-        } else {
-#pragma unroll 8
-          for (int c = 0; c < D / 8; ++c)
-            write(c, live ? __ldg(reinterpret_cast<const uint4 *>(src) + c) : make_uint4(0, 0, 0, 0));
-        }
+        const int e = exponent_of(mag);
         qs = pow2(e) * a.scale_log2;
         if (mag >= 0x7F80u) qs = __uint_as_float(0x7FC00000u);  // a non-finite query: its row is NaN throughout
         fence_proxy_async_smem();
@@ -499,8 +514,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         const float *csr = cs + st * N, *cvr = cv + st * NB * N;
         const float factor = hk.scale * qs;
         // The usual pass over TW columns: v holds their products, w receives the weights; two
-        // columns per instruction where there is a paired one.
-        auto plain = [&](const uint32_t (&v)[TW], uint32_t (&w)[TW / 2], float &sum) -> bool {
+        // columns per instruction where there is a paired one.  With `masked` the columns that the row
+        // does not see weigh nothing (their constants, folded into the operands, are finite).
+        auto plain = [&](const bool masked, int c, const uint32_t (&v)[TW], uint32_t (&w)[TW / 2], float &sum) -> bool {
+          const uint32_t from_lo = static_cast<uint32_t>(tok0 + c * TW - see_lo);  // of column 0, wrapping below
+          const uint32_t sees = static_cast<uint32_t>(max(see_hi - see_lo, 0));
+          auto shown = [&](float x, int j) { return !masked || from_lo + j < sees ? x : -INFINITY; };
           const uint64_t f2 = pair(factor, factor), shift2 = pair(e_c - ref, e_c - ref);
           uint64_t total0 = 0, total1 = 0;
           __half2 most = __float2half2_rn(0.0f);
@@ -508,7 +527,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           for (int j = 0; j < TW; j += 4) {
             const uint64_t x0 = fma2(pair_bits(v[j], v[j + 1]), f2, shift2);
             const uint64_t x1 = fma2(pair_bits(v[j + 2], v[j + 3]), f2, shift2);
-            const float p0 = ex2(low(x0)), p1 = ex2(high(x0)), p2 = ex2(low(x1)), p3 = ex2(high(x1));
+            const float p0 = ex2(shown(low(x0), j)), p1 = ex2(shown(high(x0), j + 1)), p2 = ex2(shown(low(x1), j + 2)),
+                        p3 = ex2(shown(high(x1), j + 3));
             total0 = add2(total0, pair(p0, p1));
             total1 = add2(total1, pair(p2, p3));
             w[j / 2] = pack_half2(p0, p1);
@@ -520,9 +540,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           sum = low(total0) + high(total0);
           return __low2float(most) > kMostWeight || __high2float(most) > kMostWeight;
         };
-        // A pass where some row does not see every token, where constants multiply the weights, or
-        // where a weight passed its limit: the reference is renewed if one does, and what was
-        // accumulated and weighed so far follows.
+        // A pass where constants multiply the scores or the weights, or where a weight passed its
+        // limit: the reference is renewed if one does, and what was accumulated and weighed so far
+        // follows.  (Masked steps, a tenth of those of short chunks, took this one at three times the
+        // usual pass's time: 176 us for three chunks, 1400 tokens together; 166 with a usual pass that masks.)
         auto careful = [&](int c, const uint32_t (&v)[TW], uint32_t (&w)[NB * TW / 2], float &sum) {
           float s[TW];
           float top = mx, big = rv;
@@ -595,10 +616,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           if constexpr (TW == 32) tmem_ld32(s_tmem + c * TW, v);
           else tmem_ld16(s_tmem + c * TW, v);
           tmem_ld_wait();
-          if (hide || kwide || vwide ||
-              __any_sync(0xFFFFFFFFu, plain(v, reinterpret_cast<uint32_t(&)[TW / 2]>(w), sum))) {
+          auto &usual = reinterpret_cast<uint32_t(&)[TW / 2]>(w);
+          if (kwide || vwide ||
+              __any_sync(0xFFFFFFFFu, hide ? plain(true, c, v, usual, sum)
+                                           : plain(false, c, v, usual, sum)))
             careful(c, v, w, sum);
-          }
           l = fmaf(sum, ex2(ref - e_c - mx), l);
           const uint32_t to = p_tmem + c * 32;  // over the scores just read, or apart from them
           if (!vwide) {
@@ -651,8 +673,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
                              pack_bf16x2(f[j + 4], f[j + 5]), pack_bf16x2(f[j + 6], f[j + 7]));
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<float4 *>(dst_part + k + j) = make_float4(f[j], f[j + 1], f[j + 2], f[j + 3]);
+            for (int j = 0; j < 32; j += 8)
+              st_global_v8(dst_part + k + j, f + j);  // whole sectors
           }
         }
       }
@@ -998,7 +1020,7 @@ size_t entries_of(int group, int batch, int64_t tokens) {
 template <class C>
 size_t workspace_of(int group, int batch, int64_t tokens, int num_sms) {
   const size_t e = entries_of<C>(group, batch, tokens);
-  return 16 + e * sizeof(KvEntry) + (e + 2) / 2 * 16 +
+  return 48 + e * sizeof(KvEntry) + (e + 2) / 2 * 16 +
          static_cast<size_t>(num_sms) * 2 * (sizeof(KvPart) + C::ROWS * 4 + static_cast<size_t>(C::ROWS) * C::D * 4);
 }
 
@@ -1024,7 +1046,7 @@ cudaError_t run_prefill(const KvAttnArgs &args, void *ws, int num_sms, unsigned 
   w += static_cast<size_t>(num_sms) * 2 * sizeof(KvPart);
   p.a.part_lse = reinterpret_cast<float *>(w);
   w += static_cast<size_t>(num_sms) * 2 * C::ROWS * 4;
-  p.a.part_o = reinterpret_cast<float *>(w);
+  p.a.part_o = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(w) + 31) & ~static_cast<uintptr_t>(31));  // for 32-byte stores
   if ((e = launch_k(k_kv_plan<C>, dim3(1), dim3(kPlanThreads), 0, st, 1, p)) != cudaSuccess) return e;
   if ((e = launch_k(k_kv_prefill<C>, dim3(num_sms), dim3(C::THREADS), C::SMEM_BYTES, st, 1, p)) != cudaSuccess) return e;
   return launch_k(k_kv_join<C::D, C::ROWS, 8, 1>, dim3(num_sms - 1, C::ROWS / 8), dim3(256), 0, st, 1, p.a);

@@ -516,10 +516,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         // The usual pass over TW columns: v holds their products, w receives the weights; two
         // columns per instruction where there is a paired one.  With `masked` the columns that the row
         // does not see weigh nothing (their constants, folded into the operands, are finite).
+        const uint32_t sees = static_cast<uint32_t>(max(see_hi - see_lo, 0));
+        auto seen = [&](int c, int j) { return static_cast<uint32_t>(tok0 + c * TW + j - see_lo) < sees; };
         auto plain = [&](const bool masked, int c, const uint32_t (&v)[TW], uint32_t (&w)[TW / 2], float &sum) -> bool {
-          const uint32_t from_lo = static_cast<uint32_t>(tok0 + c * TW - see_lo);  // of column 0, wrapping below
-          const uint32_t sees = static_cast<uint32_t>(max(see_hi - see_lo, 0));
-          auto shown = [&](float x, int j) { return !masked || from_lo + j < sees ? x : -INFINITY; };
+          auto shown = [&](float x, int j) { return !masked || seen(c, j) ? x : -INFINITY; };
           const uint64_t f2 = pair(factor, factor), shift2 = pair(e_c - ref, e_c - ref);
           uint64_t total0 = 0, total1 = 0;
           __half2 most = __float2half2_rn(0.0f);
@@ -540,10 +540,39 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           sum = low(total0) + high(total0);
           return __low2float(most) > kMostWeight || __high2float(most) > kMostWeight;
         };
-        // A pass where constants multiply the scores or the weights, or where a weight passed its
-        // limit: the reference is renewed if one does, and what was accumulated and weighed so far
-        // follows.  (Masked steps, a tenth of those of short chunks, took this one at three times the
-        // usual pass's time: 176 us for three chunks, 1400 tokens together; 166 with a usual pass that masks.)
+        // The reference moves: to the largest score `top` and the largest contribution `big` so far.
+        // What was accumulated, and weighed in the passes of this step before this one, follows.
+        auto renew = [&](int c, float top, float big) {
+          rv = big;
+          const float next = ceilf(fmaxf(rv - kLift, top + e_c - 100.0f));
+          const float f = next > ref ? ex2(ref - next) : 1.0f;  // a power of two
+          ref = fmaxf(ref, next);
+          l *= ex2(mx - top);
+          mx = top;
+          tmem_st_wait();
+          auto rescale = [&](uint32_t from, int cols, auto scale) {
+#pragma unroll 1
+            for (int k = 0; k < cols; k += 16) {
+              uint32_t o[16];
+              tmem_ld16(from + k, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = scale(o[j]);
+              tmem_st16(from + k, o);
+            }
+          };
+          if (step > 0)
+            rescale(o_tmem, D, [&](uint32_t x) { return __float_as_uint(__uint_as_float(x) * f); });
+          // the weights of the passes before this one (and whatever else those columns hold)
+          const __half2 f2 = __float2half2_rn(f);
+          rescale(p_tmem, c * 32, [&](uint32_t x) {
+            const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&x), f2);
+            return *reinterpret_cast<const uint32_t *>(&y);
+          });
+          tmem_st_wait();
+        };
+        // A pass where constants multiply the scores or the weights: three times the usual one's time.
+        // (Three chunks, 1400 tokens together, took 176 us when masked steps went through it as well.)
         auto careful = [&](int c, const uint32_t (&v)[TW], uint32_t (&w)[NB * TW / 2], float &sum) {
           float s[TW];
           float top = mx, big = rv;
@@ -580,33 +609,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
               for (int k = 0; k < NB; ++k) big = fmaxf(big, s[j] + lg2(cvr[k * N + c * TW + j]) + e_c);
             }
             if (!vwide) big = fmaxf(big, top + e_c);
-            rv = big;
-            const float next = ceilf(fmaxf(rv - kLift, top + e_c - 100.0f));
-            const float f = next > ref ? ex2(ref - next) : 1.0f;  // a power of two
-            ref = fmaxf(ref, next);
-            l *= ex2(mx - top);
-            mx = top;
-            tmem_st_wait();
-            auto rescale = [&](uint32_t from, int cols, auto scale) {
-#pragma unroll 1
-              for (int k = 0; k < cols; k += 16) {
-                uint32_t o[16];
-                tmem_ld16(from + k, o);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = scale(o[j]);
-                tmem_st16(from + k, o);
-              }
-            };
-            if (step > 0)
-              rescale(o_tmem, D, [&](uint32_t x) { return __float_as_uint(__uint_as_float(x) * f); });
-            // the weights of the passes before this one (and whatever else those columns hold)
-            const __half2 f2 = __float2half2_rn(f);
-            rescale(p_tmem, c * 32, [&](uint32_t x) {
-              const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&x), f2);
-              return *reinterpret_cast<const uint32_t *>(&y);
-            });
-            tmem_st_wait();
+            renew(c, top, big);
           }
         };
 #pragma unroll 1
@@ -617,10 +620,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           else tmem_ld16(s_tmem + c * TW, v);
           tmem_ld_wait();
           auto &usual = reinterpret_cast<uint32_t(&)[TW / 2]>(w);
-          if (kwide || vwide ||
-              __any_sync(0xFFFFFFFFu, hide ? plain(true, c, v, usual, sum)
-                                           : plain(false, c, v, usual, sum)))
+          if (kwide || vwide) {
             careful(c, v, w, sum);
+          } else if (__any_sync(0xFFFFFFFFu, hide ? plain(true, c, v, usual, sum) : plain(false, c, v, usual, sum))) {
+            float most = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < TW; ++j)
+              if (!hide || seen(c, j)) most = fmaxf(most, __uint_as_float(v[j]));
+            const float top = fmaxf(mx, most * factor);
+            renew(c, top, fmaxf(rv, top + e_c));
+            plain(true, c, v, usual, sum);
+          }
           l = fmaf(sum, ex2(ref - e_c - mx), l);
           const uint32_t to = p_tmem + c * 32;  // over the scores just read, or apart from them
           if (!vwide) {

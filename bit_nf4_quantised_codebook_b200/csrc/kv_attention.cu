@@ -744,9 +744,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
       auto group_of = [&](int64_t u) { return static_cast<int>(((u + 1) * workers - 1) / total); };
       KvPart p;
       p.present = 1;
-      p.b = b;
+      p.row0 = sp.q.row0;
       p.head = head;
       p.tile = tile;
+      p.rows = row_limit;
       p.g0 = group_of(first + kItemOverhead);  // holds the item's first step
       p.last = group_of(end - 1);
       p.head_slot = p.g0 * total / workers >= first ? 0 : 1;
@@ -764,6 +765,7 @@ using Cfg128x1 = AttnCfg<128, 1, 4>;
 using Cfg128x2 = AttnCfg<128, 2, 3>;
 using Cfg256x1 = AttnCfg<256, 1, 3>;
 
+constexpr int kManyParts = 8;
 template <class C>
 cudaError_t run_attention(KvAttnArgs a, void *ws, int num_sms, cudaStream_t st) {
   static std::atomic<uint64_t> attr_done{0};
@@ -779,7 +781,13 @@ cudaError_t run_attention(KvAttnArgs a, void *ws, int num_sms, cudaStream_t st) 
   a.part_o = reinterpret_cast<float *>(w);
   e = launch_k(k_kv_attention<C>, dim3(num_sms), dim3(C::THREADS), C::SMEM_BYTES, st, 1, a);
   if (e != cudaSuccess) return e;
-  return launch_k(k_kv_join<C::D, C::ROWS, 2, 4>, dim3(workers - 1, C::ROWS / 2), dim3(256), 0, st, 1, a);
+  // Four warps to a row where an item has many parts (one sequence of 131071 tokens, 74 parts to
+  // an item: 49 against 54 us); one where it has a few, in a quarter of the CTAs, most of which find
+  // nothing to join (24 sequences of drafts: 22 against 27 us).  With the many-row kernel in the
+  // call there is usually nothing at all.
+  if (a.few_rows == INT_MAX && workers > kManyParts * static_cast<int64_t>(a.kb.batch) * a.heads)
+    return launch_k(k_kv_join<C::D, C::ROWS, 4>, dim3(workers - 1, C::ROWS / 2), dim3(256), 0, st, 1, a);
+  return launch_k(k_kv_join<C::D, C::ROWS, 1>, dim3(workers - 1, C::ROWS / 8), dim3(256), 0, st, 1, a);
 }
 
 template <class C>

@@ -38,12 +38,14 @@ struct KvAttnArgs {
 
 // A worker's part of an item that it shares with others (slot 0: the item its range
 // starts in; slot 1: the one it ends in).
-struct KvPart {
+struct alignas(16) KvPart {
   int present;
-  int b, head, tile;
+  int joins;      // 1: the second part of its item, whose CTA joins them all
   int g0, last;   // the item's first and last worker
   int head_slot;  // slot of the first worker's part
-  int joins;      // 1: the second part of its item, whose CTA joins them all
+  int row0;       // first token row of the sequence
+  int head, tile;
+  int rows;       // of the tile
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -80,24 +82,23 @@ template <int N>  // all but the last N groups of this thread's copies have land
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// Joins the items that several workers shared.  CTA (k, y): WARPS rows, SPLIT warps to each, of the
-// item that the range of worker k starts inside of, when worker k holds the item's second
-// part.  The parts' weights come first, all at once; then the parts, eight loads in flight.
+// Joins the items that several workers shared.  CTA (k, y): 8 / SPLIT rows, SPLIT warps to each, of
+// the item that the range of worker k starts inside of, when worker k holds the item's second
+// part.  The first parts are loaded together with all the weights.
 constexpr int kMaxWorkers = 1024;
-template <int D, int ROWS, int WARPS, int SPLIT>
-__global__ void __launch_bounds__(WARPS * SPLIT * 32) k_kv_join(const __grid_constant__ KvAttnArgs a) {
+template <int D, int ROWS, int SPLIT>
+__global__ void __launch_bounds__(256) k_kv_join(const __grid_constant__ KvAttnArgs a) {
   constexpr int V = D / 32;  // channels per lane
-  __shared__ float s_acc[SPLIT > 1 ? WARPS * SPLIT * D : 1];
+  constexpr int U = SPLIT > 1 ? 8 : 4;  // loads in flight, of parts
+  __shared__ float s_acc[SPLIT > 1 ? 8 * D : 1];
   pdl_wait();
   pdl_launch_dependents();
   const int k = static_cast<int>(blockIdx.x) + 1;
   const KvPart p = a.parts[k * 2];
   if (!p.joins) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp % SPLIT;
-  const int r = static_cast<int>(blockIdx.y) * WARPS + warp / SPLIT;
-  const KvSeq q = kv_seq(a.kb, p.b);
-  const int rr = p.tile * ROWS + r;
-  const bool live = rr < q.n * a.group;
+  const int r = static_cast<int>(blockIdx.y) * (8 / SPLIT) + warp / SPLIT;
+  const bool live = r < p.rows;
   if (SPLIT == 1 && !live) return;
   const int n = live ? p.last - p.g0 + 1 : 0;
   auto part_of = [&](int i) { return static_cast<int64_t>(p.g0 + i) * 2 + (i == 0 ? p.head_slot : 0); };
@@ -105,46 +106,46 @@ __global__ void __launch_bounds__(WARPS * SPLIT * 32) k_kv_join(const __grid_con
     const int64_t part = part_of(i);
     return a.parts[part].present ? a.part_lse[part * ROWS + r] : -INFINITY;  // workers without steps
   };
+  // this warp's parts: share, share + SPLIT, ...
+  const int mine = (n - share + SPLIT - 1) / SPLIT;
+  float2 v[U][V / 2];
+  auto load = [&](int j0) {
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const int i = share + min(j0 + j, mine - 1) * SPLIT;
+      const float *src = a.part_o + (part_of(i) * ROWS + r) * D + lane * V;
+#pragma unroll
+      for (int x = 0; x < V / 2; ++x) v[j][x] = *reinterpret_cast<const float2 *>(src + 2 * x);
+    }
+  };
+  if (mine > 0) load(0);
   float top = -INFINITY;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, lse_of(i));
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
   float sum = 0.0f, acc[V] = {};
-  // this warp's parts: share, share + SPLIT, ...
-  const int mine = (n - share + SPLIT - 1) / SPLIT;
   for (int i = lane; i < n; i += 32) {
     const float lse = lse_of(i);
     sum += lse == -INFINITY ? 0.0f : ex2(lse - top);
   }
-  for (int base = 0; base < mine; base += 32) {
-    float weight = 0.0f;
-    if (base + lane < mine) {
-      const float lse = lse_of(share + (base + lane) * SPLIT);
+  float weight = 0.0f;
+  for (int j0 = 0; j0 < mine; j0 += U) {
+    if ((j0 & 31) == 0 && j0 + lane < mine) {  // (what lanes past the last part hold is not used)
+      const float lse = lse_of(share + (j0 + lane) * SPLIT);
       weight = lse == -INFINITY ? 0.0f : ex2(lse - top);
     }
-    const int here = min(32, mine - base);
-    constexpr int U = 8;
-    for (int j0 = 0; j0 < here; j0 += U) {
-      float2 v[U][V / 2];
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int i = share + (base + min(j0 + j, here - 1)) * SPLIT;
-        const float *src = a.part_o + (part_of(i) * ROWS + r) * D + lane * V;
+    for (int j = 0; j < U; ++j) {
+      const float f = __shfl_sync(0xFFFFFFFFu, weight, (j0 + j) & 31);
+      if (j0 + j < mine && f != 0.0f) {  // an absent part holds anything
 #pragma unroll
-        for (int x = 0; x < V / 2; ++x) v[j][x] = *reinterpret_cast<const float2 *>(src + 2 * x);
-      }
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const float f = __shfl_sync(0xFFFFFFFFu, weight, (j0 + j) & 31);
-        if (j0 + j < here && f != 0.0f) {  // an absent part holds anything
-#pragma unroll
-          for (int x = 0; x < V / 2; ++x) {
-            acc[2 * x] = fmaf(f, v[j][x].x, acc[2 * x]);
-            acc[2 * x + 1] = fmaf(f, v[j][x].y, acc[2 * x + 1]);
-          }
+        for (int x = 0; x < V / 2; ++x) {
+          acc[2 * x] = fmaf(f, v[j][x].x, acc[2 * x]);
+          acc[2 * x + 1] = fmaf(f, v[j][x].y, acc[2 * x + 1]);
         }
       }
     }
+    if (j0 + U < mine) load(j0 + U);
   }
 #pragma unroll
   for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
@@ -159,8 +160,8 @@ __global__ void __launch_bounds__(WARPS * SPLIT * 32) k_kv_join(const __grid_con
       for (int x = 0; x < V; ++x) acc[x] += s_acc[(warp + w) * D + lane * V + x];
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int i = rr / a.group, h = rr - i * a.group;
-  uint16_t *dst = a.out + ((static_cast<int64_t>(q.row0 + i) * a.heads + p.head) * a.group + h) * D + lane * V;
+  const int rr = p.tile * ROWS + r, i = rr / a.group, h = rr - i * a.group;
+  uint16_t *dst = a.out + ((static_cast<int64_t>(p.row0 + i) * a.heads + p.head) * a.group + h) * D + lane * V;
 #pragma unroll
   for (int x = 0; x < V / 2; ++x)
     *reinterpret_cast<uint32_t *>(dst + 2 * x) = pack_bf16x2(acc[2 * x] * inv, acc[2 * x + 1] * inv);

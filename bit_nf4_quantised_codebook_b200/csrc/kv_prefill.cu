@@ -698,9 +698,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           auto worker_of = [&](int64_t u) { return static_cast<int>(((u + 1) * workers - 1) / total); };
           KvPart kp;
           kp.present = 1;
-          kp.b = sg.b;
+          kp.row0 = sg.q.row0;
           kp.head = sg.head;
           kp.tile = sg.tile;
+          kp.rows = sg.rows;
           kp.g0 = worker_of(sg.first + kItemOverhead);  // holds the item's first step
           kp.last = worker_of(sg.end - 1);
           kp.head_slot = kp.g0 * total / workers >= sg.first ? 0 : 1;
@@ -1059,7 +1060,7 @@ cudaError_t run_prefill(const KvAttnArgs &args, void *ws, int num_sms, unsigned 
   p.a.part_o = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(w) + 31) & ~static_cast<uintptr_t>(31));  // for 32-byte stores
   if ((e = launch_k(k_kv_plan<C>, dim3(1), dim3(kPlanThreads), 0, st, 1, p)) != cudaSuccess) return e;
   if ((e = launch_k(k_kv_prefill<C>, dim3(num_sms), dim3(C::THREADS), C::SMEM_BYTES, st, 1, p)) != cudaSuccess) return e;
-  return launch_k(k_kv_join<C::D, C::ROWS, 8, 1>, dim3(num_sms - 1, C::ROWS / 8), dim3(256), 0, st, 1, p.a);
+  return launch_k(k_kv_join<C::D, C::ROWS, 1>, dim3(num_sms - 1, C::ROWS / 8), dim3(256), 0, st, 1, p.a);
 }
 
 }  // namespace

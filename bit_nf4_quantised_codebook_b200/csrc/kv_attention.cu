@@ -179,11 +179,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gq = warp >> 2, gw = warp & 3;  // group in the CTA, warp in the group
   const int g = lane >> 2, t = lane & 3;
-  for (int i = tid; i < 256 * 32; i += C::THREADS) {
-    const int byte = i >> 5;
-    const __half2 h = __halves2half2(a.levels[byte >> 4], a.levels[byte & 15]);
-    *reinterpret_cast<__half2 *>(smem + (table - smem_base) + byte * 256 + (i & 31) * 4) = h;
-  }
+  auto build_table = [&] {
+    for (int i = tid; i < 256 * 32; i += C::THREADS) {
+      const int byte = i >> 5;
+      const __half2 h = __halves2half2(a.levels[byte >> 4], a.levels[byte & 15]);
+      *reinterpret_cast<__half2 *>(smem + (table - smem_base) + byte * 256 + (i & 31) * 4) = h;
+    }
+  };
+  // beside the many-row kernel there is often nothing to do here, and no kernel before this one
+  // leaves room to build the table while it runs
+  const bool alone = a.few_rows == INT_MAX;
+  if (alone) build_table();
   pdl_wait();
   pdl_launch_dependents();
   if (table - smem_base < C::FRONT * C::RING) {  // cannot happen while shared memory starts low
@@ -214,6 +220,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
     __syncthreads();
   }
   int64_t total = prefix[C::THREADS];
+  if (!alone && total > 0) {
+    build_table();
+    __syncthreads();
+  }
   const int workers = gridDim.x * C::GROUPS, me = blockIdx.x * C::GROUPS + gq;
   int64_t at = me * total / workers;
   int64_t stop = static_cast<int64_t>(me + 1) * total / workers;

@@ -89,7 +89,7 @@ constexpr int kMaxWorkers = 1024;
 template <int D, int ROWS, int SPLIT>
 __global__ void __launch_bounds__(256) k_kv_join(const __grid_constant__ KvAttnArgs a) {
   constexpr int V = D / 32;  // channels per lane
-  constexpr int U = SPLIT > 1 ? 8 : 4;  // loads in flight, of parts
+  constexpr int U = SPLIT > 1 || ROWS < 128 ? 4 : 2;  // parts loaded at once (those of the long items of prompts are two or three)
   __shared__ float s_acc[SPLIT > 1 ? 8 * D : 1];
   pdl_wait();
   pdl_launch_dependents();

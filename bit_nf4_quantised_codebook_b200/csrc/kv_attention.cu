@@ -40,7 +40,7 @@
 // Bound by the issue of the decoding: 2.9 instructions per element (one of them the lookup
 // and permute of a pair's half, a quarter the copies and the softmax), load/store pipe 68 %
 // and integer pipe 49 % busy.  64 sequences of 1 to 8192 tokens, 64 query and 8 key/value
-// heads of 128: 87 us, 3.45 TB/s of codes and constants (0.54 of the measured copy rate); one
+// heads of 128: 81 us, 3.73 TB/s of codes and constants (0.58 of the measured copy rate); one
 // sequence of 131071: 49 us.  Codes loaded straight into registers took 62 us for the latter
 // (one 32-byte sector per request), registers spilled beside a full shared memory 4 us.
 #include <atomic>
@@ -59,7 +59,7 @@ namespace {
 constexpr int kStepTokens = 128;     // tokens of one step of a group (4 warps x 32)
 // What starting and ending an item costs a group, in steps: its place on the line is that much
 // longer than its steps, so that a group with many short items gets fewer of them.
-constexpr int kItemOverhead = 3;  // 64 uneven sequences: 112 us without, 98, 87, 87, 89 us with 1, 2, 3, 5
+constexpr int kItemOverhead = 3;  // 64 uneven sequences: 106 us without, 92, 81, 81, 83 us with 1, 2, 3, 5
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -818,16 +818,22 @@ size_t few_workspace(int head_dim, int num_sms) {
 // Sequences with more rows (tokens x query heads per key/value head) than this go to the
 // many-row kernel.
 constexpr int kFewRows = 64;
-// The host does not know how a call's rows are spread.  If every sequence has one token or
-// more, none has more than tokens - batch + 1: up to that many rows above one token each, the
-// few-row kernel takes the whole call (right for any number of rows, each 16 of them decoding
-// the cache anew).  Measured: the many-row kernel's launches cost a call without use for them
-// 11 us (64 single tokens over 2800 on average, 8 rows each: 117 against 128 us).
-// Single tokens stay here for any number of query heads too: with 128 of them on one key/value
-// head, one sequence of 32768 tokens takes 32 us (many-row kernel: 71), 16 of 4096 48 us (45); only
-// 64 of 2048 would be better off there (81 against 59 us).
+// The host knows a call's totals, not how its rows are spread.  The many-row kernels are launched
+// where the sequences have more than kFewRows on average (one sequence over 16384 cached tokens, 8
+// key/value heads: 132 rows 54 us against 74 in the few-row kernel, 68 rows 48 against 49; over 2048
+// tokens 32 against 27 and 28 against 23), or where one of them may have many: if each has one token or
+// more, none has more rows than its first token's and those above one token each.  Up to kSpreadRows
+// of those, the few-row kernel takes the whole call (right for any number of rows, each 16 of
+// them decoding the cache anew): the launches cost a call without use for them 11 us (16 sequences of
+// 4096 tokens, 40 rows each: 107 against 96 us).
+// Single tokens stay in the few-row kernel for any number of query heads: with 128 of them on one
+// key/value head, one sequence of 32768 tokens takes 32 us (many-row kernel: 71), 16 of 4096 48 us
+// (45); only 64 of 2048 would be better off there (81 against 59 us).
 constexpr int64_t kSpreadRows = 512;
-bool may_have_many_rows(int64_t tokens, int batch, int group) { return (tokens - batch) * group > kSpreadRows; }
+bool may_have_many_rows(int64_t tokens, int batch, int group) {
+  const int64_t more = (tokens - batch) * group;
+  return more > kSpreadRows || (more > 0 && tokens * group > static_cast<int64_t>(kFewRows) * batch);
+}
 }  // namespace
 
 size_t kv_attention_workspace(int head_dim, int group, int batch, int64_t tokens, int num_sms) {

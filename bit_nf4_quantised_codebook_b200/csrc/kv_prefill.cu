@@ -29,14 +29,15 @@
 // weights are 2^(s - r), r renewed when one passes 2^14: the largest then weighs 2^6, and what
 // is 2^-31 of it vanishes (its value can be 2^8 times another's of the step: 2^-23).
 //
-// Measured (4096 tokens x 4 query heads over 8192 cached, 8 key/value heads of 128): 0.59 ms,
-// 696 TFLOP/s of the visible pairs.  A step takes 5600 clocks, of which the tensor cores work
-// 2100: it is bound by the chain from one step of a row tile to the next (softmax 3150 clocks,
-// the two products and their hand-overs 1800) and by the decoding of the values between two
-// products that use them (2400).  Tried without gain: values in two stages (more decoding next
-// to the softmax slows it as much), scores in two halves (products of 64 columns), 20 warps,
-// two passes of the softmax between checks (spills, and with shared memory full a spilled
-// register is a second-level cache access).
+// Measured (4096 tokens x 4 query heads over 8192 cached, 8 key/value heads of 128): 0.56 ms,
+// 739 TFLOP/s of the visible pairs.  A step takes 5200 clocks, of which the tensor cores work
+// 2100: it is bound by the chain from one step of a row tile to the next (softmax, the two
+// products and their hand-overs) and by the decoding of the values between two products that use
+// them (2400).  An item starts and ends in 15000 clocks (queries, first keys, outputs), the kernel in
+// 10000.  Tried without gain: values in two stages (more decoding next to the softmax slows it as
+// much), scores in two halves (products of 64 columns), 20 warps, two passes of the softmax between
+// checks (spills, and with shared memory full a spilled register is a second-level cache access),
+// outputs turned through shared memory (the stores are faster, the steps slower).
 #include <atomic>
 #include <cstdint>
 #include <cuda_fp16.h>
@@ -81,7 +82,7 @@ struct PreCfg {
 // weight that vanishes in fp16 (2^-31 of the largest) can have a value 2^8 times another's.
 constexpr int kNearKeys = 12, kNearValues = 8;
 // What starting and ending an item costs a CTA, in steps: part of its place on the line.
-constexpr int kItemOverhead = 2;
+constexpr int kItemOverhead = 2;  // three chunks, 1400 tokens together: 152, 146, 148, 146 us with 1, 2, 3, 4
 constexpr unsigned long long kDrainNs = 1000000000ull;  // bound on the wait for the MMAs in flight at the end
 
 // How a step's keys and values were written (by the decoding warps, for the others).  Where

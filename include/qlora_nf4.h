@@ -453,8 +453,9 @@ qlora_status qlora_kv_append(const qlora_kv_cache *cache, const qlora_kv_batch *
 qlora_status qlora_kv_read(const qlora_kv_cache *cache, const qlora_kv_batch *batch, uint16_t *K_out,
                            uint16_t *V_out, int *dev_err, void *stream);
 
-/* Workspace bytes of qlora_kv_attention (16-byte aligned, holds no state
- * between calls; calls that may overlap need one each). */
+/* Workspace bytes of a qlora_kv_attention call of these sizes (16-byte aligned,
+ * holds no state between calls; calls that may overlap need one each).  For a
+ * given batch it grows with tokens; fewer sequences may need more. */
 qlora_status qlora_kv_attention_workspace_size(const qlora_kv_cache *cache, int batch, int64_t tokens, int q_heads,
                                                size_t *bytes);
 

@@ -10,7 +10,7 @@
 // two units of both sides, all loads issued together.
 // Bound by HBM for prompts (2 + 17/32 bytes per element each way) and by the chain of
 // dependent loads token_start -> kv_len -> page_table -> data for single tokens.  Measured:
-// reading 60000 tokens of 8 heads of 128 takes 56 us (5.5 TB/s, 0.86 of the measured copy
+// reading 60000 tokens of 8 heads of 128 takes 56 us (5.5 TB/s, 0.85 of the measured copy
 // rate); appending 8000 such tokens and reading them back 25 us (3.6 TB/s, the append bound by
 // 25 instructions per element); a step of 16 tokens of 32 heads 5 us for both.
 //

@@ -97,6 +97,21 @@ def test_long_prompt():
     _run(Case([1500], [2100], page_size=64, seed=5), 1, 4, 128)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_items_of_many_parts(dim):
+    """A long cache under a single token and under a chunk of two row tiles, in one call: each item is
+    shared by more workers than a warp has lanes."""
+    _run(Case([1, 100, 1], [20_011, 20_500, 3], page_size=128, pad=1, seed=21), 1, 4, dim)
+
+
+@pytest.mark.parametrize("others", [0, 5])
+@pytest.mark.parametrize("n", [2, 16, 17, 32, 33, 129, 130])
+def test_rows_around_the_limits_between_kernels(n, others):
+    """64 rows and 512 of four query heads each are where the choice of kernel changes; alone, and beside single
+    tokens and empty sequences."""
+    _run(Case([n] + [1, 0, 1, 1, 0][:others], [n + 100] + [70, 9, 300, 1, 0][:others], page_size=32, seed=22), 2, 4, 128)
+
+
 def test_many_sequences():
     n = [b % 3 % 2 for b in range(4096)]
     case = Case(n, [(5 * b) % 23 + x for b, x in enumerate(n)], page_size=16, pad=2, seed=6)
@@ -330,6 +345,31 @@ def test_decode_loop_in_a_graph():
                 state[b][s] = np.concatenate([state[b][s], kv.decode(codes, absmax, "nf4")[None]])
         now = Case([1, 1], lens, page_size=16)
         _verify(now, {b: tuple(state[b]) for b in state}, Q, out, dim ** -0.5, True, 0, "nf4")
+
+
+def test_prompt_chunks_in_a_graph():
+    """A captured call (on the capture's own stream) gives the bits of a direct one, and follows the batch
+    arrays when they are rewritten."""
+    a = api()
+    case = Case([200, 1, 90], [700, 300, 400], page_size=64, pad=2, seed=23)
+    c, mirror = filled_cache(a, case, 2, 128, "nf4", np.random.default_rng(98))
+    Q = bf16(np.random.default_rng(99).standard_normal((case.tokens, 8, 128))).cuda()
+    batch = case.batch(a)
+    out = torch.zeros(case.tokens, 8, 128, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(a.qlora_kv_attention_workspace_size(c, 3, case.tokens, 8), dtype=torch.uint8, device="cuda")
+    err = a.new_error_word()
+    a.qlora_kv_attention(c, batch, Q, out=out, ws=ws, dev_err=err)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.qlora_kv_attention(c, batch, Q, out=out, ws=ws, dev_err=err)
+    for shorter in (0, 130):
+        batch.kv_len.sub_(shorter)
+        graph.replay()
+        graph.replay()
+        got = out.clone()
+        direct = a.qlora_kv_attention(c, batch, Q)
+        assert np.array_equal(bits(got)[: case.tokens - case.pad], bits(direct)[: case.tokens - case.pad])
+    check_dev_err(err)
 
 
 def test_pool_larger_than_4_gib():

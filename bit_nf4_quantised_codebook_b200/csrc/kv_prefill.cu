@@ -565,9 +565,10 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           if (step > 0)
             rescale(o_tmem, D, [&](uint32_t x) { return __float_as_uint(__uint_as_float(x) * f); });
           // the weights of the passes before this one (and whatever else those columns hold)
-          const __half2 f2 = __float2half2_rn(f);
+          // (by two factors: below 2^-24 one would be 0 in fp16, with weights of 2^14 before it)
+          const __half2 f2 = __float2half2_rn(fmaxf(f, 0x1p-24f)), rest = __float2half2_rn(f < 0x1p-24f ? f * 0x1p24f : 1.0f);
           rescale(p_tmem, c * 32, [&](uint32_t x) {
-            const __half2 y = __hmul2(*reinterpret_cast<__half2 *>(&x), f2);
+            const __half2 y = __hmul2(__hmul2(*reinterpret_cast<__half2 *>(&x), f2), rest);
             return *reinterpret_cast<const uint32_t *>(&y);
           });
           tmem_st_wait();

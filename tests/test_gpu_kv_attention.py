@@ -162,6 +162,32 @@ def test_values_of_any_size(dim, n):
     _constants_of_any_size(dim, n, "v", rng.integers(-9, 1, 90))
 
 
+@pytest.mark.parametrize("n", [2, 40])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_maximum_that_jumps_within_a_step(dim, n):
+    """The scores of one step rise by 7 binades after a quarter of it and by 18 more after three quarters:
+    what was weighed before has weights of 2^-18 then, but there are many and their values 2^7 times the
+    last ones' (1/32 of the output; with 256 channels and steps half as long, 1/64)."""
+    a = api()
+    quarter = 16 if dim == 256 else 32
+    case = Case([n], [4 * quarter], page_size=16, seed=24)
+    c, _ = filled_cache(a, case, 1, dim, "int4", np.random.default_rng(1))
+    kc, vc = np.full(4 * quarter, 1.0), np.full(4 * quarter, 1.0)
+    kc[quarter:3 * quarter], vc[quarter:3 * quarter] = 1.21875, 128.0  # 7 / 32 more
+    kc[3 * quarter + 5] = 1.78125                                     # 25 / 32 more
+    K, V = (np.repeat(x[:, None, None], dim, axis=2) for x in (kc, vc))
+    whole = Case([4 * quarter], [4 * quarter], page_size=16, seed=24)
+    whole.table = case.table
+    a.qlora_kv_append(c, whole.batch(a), bf16(K).cuda(), bf16(V).cuda())
+    Q = torch.ones(n, 2, dim, dtype=torch.bfloat16, device="cuda")
+    scale = float(np.float32(32 * np.log(2) / dim))
+    out = a.qlora_kv_attention(c, case.batch(a), Q, scale=scale, causal=False)
+    want, bound = kv.attention(f64(Q), K, V, scale, False, 0, False)
+    assert bound.max() < np.abs(want - 1).min()  # tells them from nothing
+    off = (np.abs(f64(out) - want) - bound).max()
+    assert off <= 0, off
+
+
 @pytest.mark.parametrize("n", [2, 60])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_keys_of_any_size(dim, n):

@@ -30,7 +30,7 @@
 // is 2^-31 of it vanishes (its value can be 2^8 times another's of the step: 2^-23).
 //
 // Measured (4096 tokens x 4 query heads over 8192 cached, 8 key/value heads of 128): 0.56 ms,
-// 739 TFLOP/s of the visible pairs.  A step takes 5200 clocks, of which the tensor cores work
+// 742 TFLOP/s of the visible pairs.  A step takes 5200 clocks, of which the tensor cores work
 // 2100: it is bound by the chain from one step of a row tile to the next (softmax, the two
 // products and their hand-overs) and by the decoding of the values between two products that use
 // them (2400).  An item starts and ends in 15000 clocks (queries, first keys, outputs), the kernel in

@@ -550,7 +550,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_attention(const __grid_con
 #pragma unroll
               for (int k = 0; k < NB; ++k) {
                 const float cv = const_of<NB>(vcon[i][x], k);
-                float w0 = p0 * (cv * fv[n][k][0]), w1 = p1 * (cv * fv[n][k][1]);
+                // (in this order: a scale times a constant may pass float32, and 0 * inf would stay)
+                float w0 = p0 * cv * fv[n][k][0], w1 = p1 * cv * fv[n][k][1];
                 if (hide) {  // a token that a row does not see adds nothing, whatever its value's constant
                   w0 = s0 == -INFINITY ? 0.0f : w0;
                   w1 = s1 == -INFINITY ? 0.0f : w1;

@@ -1,0 +1,90 @@
+"""GPU parity of qlora_kv_attention where the values' constants and the scores lie far
+apart: zero blocks of values under high scores, steps of very different sizes, blocks of
+one head of very different sizes, peaked softmax.
+
+The inputs are exact in every format on the way (Int4 codes +-7, constants that are
+bfloat16 numbers, queries of ones), so the oracle's bound is a few parts in a thousand of
+what the visible values weigh, and tells a right output from a wrong one."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv
+from tests.gpu_util import api, check_dev_err
+from tests.kv_util import Case, bf16, f64
+
+pytestmark = pytest.mark.gpu
+
+DIMS = [64, 128, 256]
+
+
+def _step(dim):
+    """Cached tokens that the many-row kernel weighs together."""
+    return 64 if dim == 256 else 128
+
+
+def _fill(a, t, size, heads, dim, signs, case):
+    """A cache with one sequence: the keys of token j give every row the score t[j] (in powers of two),
+    its values are size[j, block] with a sign per channel; every head the same."""
+    length = len(t)
+    c = a.alloc_kv_cache(case.num_pages, heads, dim, case.page_size, "int4")
+    whole = Case([length], [length], page_size=case.page_size)
+    whole.table = case.table[:1]
+    K = np.repeat(np.asarray(t, np.float64)[:, None, None], dim, axis=2)
+    V = (np.repeat(np.asarray(size, np.float64), 64, axis=1) * signs)[:, None]
+    for x in (K, V):
+        assert np.array_equal(f64(bf16(x)), x)
+    a.qlora_kv_append(c, whole.batch(a), *(bf16(x).cuda().expand(-1, heads, -1) for x in (K, V)))
+    return c, K, V
+
+
+def _scale(dim):
+    return float(np.float32(np.log(2.0) / dim))
+
+
+def _off(out, K, V, dim, extra=0.0):
+    """How far past its bound the furthest output is; every row and head sees the same."""
+    want, bound = kv.attention(np.ones((1, 1, dim)), K, V, _scale(dim), False, 0, False)
+    got = f64(out)
+    assert np.all(np.isfinite(got)), "non-finite output"
+    return (np.abs(got - want) - bound - extra).max(), want, bound
+
+
+def _run(t, size, n, heads, group, dim, extra=0.0):
+    a = api()
+    signs = np.where(np.random.default_rng(len(t)).random(dim) < 0.5, -1.0, 1.0)
+    case = Case([n], [len(t)], page_size=16, seed=30)
+    c, K, V = _fill(a, t, size, heads, dim, signs, case)
+    Q = torch.ones(n, heads * group, dim, dtype=torch.bfloat16, device="cuda")
+    err = a.new_error_word()
+    out = a.qlora_kv_attention(c, case.batch(a), Q, scale=_scale(dim), causal=False, dev_err=err)
+    check_dev_err(err)
+    off, want, bound = _off(out, K, V, dim, extra)
+    assert off <= 0, off
+    return want, bound
+
+
+def _near(rng, length, spread=2.0):
+    """Scores that differ by a few binades (sixteenths: exact in bfloat16)."""
+    return np.round(rng.uniform(-spread, spread, length) * 16) / 16
+
+
+@pytest.mark.parametrize("n", [1, 2, 60])
+@pytest.mark.parametrize("dim", DIMS)
+def test_zero_values_under_the_highest_score(dim, n):
+    """The token with the highest score has an all-zero block of values; the others' weights lie 130
+    binades below and vanish in float32 (a weight below 2^-126 of the largest: `extra`)."""
+    for size in (2.0, 4.0, 2.0 ** 20, 2.0 ** 100):
+        t, values = np.full(90, -130.0), np.full((90, dim // 64), size)
+        t[7], values[7] = 0.0, 1.0
+        values[7, 0] = 0.0
+        _run(t, values, n, 2, 4, dim, extra=90 * 2.0 ** -126 * size)
+
+
+@pytest.mark.parametrize("n", [1, 2, 60])
+@pytest.mark.parametrize("dim", DIMS)
+def test_huge_value_far_below_the_highest_score(dim, n):
+    """A value of 2^123 whose weight, 2^-150, vanishes in float32 beside ordinary tokens."""
+    t, values = _near(np.random.default_rng(31), 90), np.ones((90, dim // 64))
+    t[40], values[40] = -150.0, 2.0 ** 123
+    _run(t, values, n, 2, 4, dim, extra=2.0 ** (123 - 148))

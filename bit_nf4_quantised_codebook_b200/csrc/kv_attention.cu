@@ -113,7 +113,8 @@ __device__ __forceinline__ KvSpan kv_span(const KvAttnArgs &a, int b, int tile_r
   KvSpan s;
   s.q = kv_seq(a.kb, b);
   const int rows = s.q.n * a.group;
-  s.tiles = rows > a.few_rows ? 0 : (rows + tile_rows - 1) / tile_rows;
+  // (written by an earlier kernel of this call, maybe after this one started: from the second-level cache)
+  s.tiles = rows > a.few_rows && __ldcg(a.again + b) == 0 ? 0 : (rows + tile_rows - 1) / tile_rows;
   int lo = 0;
   if (a.window > 0) lo = max(0, min(s.q.len, s.q.pos0() - a.window + 1)) & ~31;
   s.lo = lo;
@@ -835,11 +836,13 @@ bool may_have_many_rows(int64_t tokens, int batch, int group) {
   const int64_t more = (tokens - batch) * group;
   return more > kSpreadRows || (more > 0 && tokens * group > static_cast<int64_t>(kFewRows) * batch);
 }
+size_t again_bytes(int batch) { return (static_cast<size_t>(batch) * 4 + 15) / 16 * 16; }
 }  // namespace
 
 size_t kv_attention_workspace(int head_dim, int group, int batch, int64_t tokens, int num_sms) {
   size_t bytes = (few_workspace(head_dim, num_sms) + 15) / 16 * 16;
-  if (may_have_many_rows(tokens, batch, group)) bytes += kv_prefill_workspace(head_dim, group, batch, tokens, num_sms);
+  if (may_have_many_rows(tokens, batch, group))
+    bytes += again_bytes(batch) + kv_prefill_workspace(head_dim, group, batch, tokens, num_sms);
   return bytes;
 }
 
@@ -884,7 +887,9 @@ cudaError_t launch_kv_attention(const qlora_kv_cache &c, const KvBatch &kb, cons
   if (may_have_many_rows(kb.tokens, kb.batch, a.group)) {
     a.few_rows = kFewRows;
     uint8_t *more = static_cast<uint8_t *>(ws) + (few_workspace(c.head_dim, num_sms) + 15) / 16 * 16;
-    const cudaError_t e = launch_kv_prefill(a, c.head_dim, more, num_sms, timeout_ns, st);
+    a.again = reinterpret_cast<int32_t *>(more);
+    const cudaError_t e =
+        launch_kv_prefill(a, c.head_dim, more + again_bytes(kb.batch), num_sms, timeout_ns, st);
     if (e != cudaSuccess) return e;
   }
   // 16-row tiles once a sequence has on average more than 8 rows per key/value head (a

@@ -29,6 +29,7 @@ struct KvAttnArgs {
   float v_unit;       // 1 / unit: levels are stored times `unit`
   int causal, window;
   int few_rows;       // sequences with more rows (tokens x group) than this go to the many-row kernel
+  int32_t *again;     // [batch] those that it leaves to the few-row kernel all the same (with few_rows only)
   __half levels[16];
   // workspace
   float *part_o;      // [workers][2][rows of a tile][D] normalised partial outputs

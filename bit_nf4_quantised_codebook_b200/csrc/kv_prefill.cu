@@ -28,6 +28,10 @@
 // float32; and one more rounding of level x constant to fp16 (2^-11) for NF4.  A row's
 // weights are 2^(s - r), r renewed when one passes 2^14: the largest then weighs 2^6, and what
 // is 2^-31 of it vanishes (its value can be 2^8 times another's of the step: 2^-23).
+// The weights carry their step's exponent, and so does their sum, which is brought to the
+// row's maximum before it is added: where a step's values are so small beside what the row has
+// seen that the sum would lose terms (kFar), the sequence is marked in `again`, and the few-row kernel,
+// launched behind this one, whose sums know nothing of the values, computes it anew.
 //
 // Measured (4096 tokens x 4 query heads over 8192 cached, 8 key/value heads of 128): 0.56 ms,
 // 742 TFLOP/s of the visible pairs.  A step takes 5200 clocks, of which the tensor cores work
@@ -83,6 +87,10 @@ struct PreCfg {
 constexpr int kNearKeys = 12, kNearValues = 8;
 // What starting and ending an item costs a CTA, in steps: part of its place on the line.
 constexpr int kItemOverhead = 2;  // three chunks, 1400 tokens together: 152, 146, 148, 146 us with 1, 2, 3, 4
+// Binades between the unit of a step's sum and the row's largest weight: of 126 in float32, so that what is
+// lost is 2^-62 of that weight or less.  Ordinary steps stay below 10.
+constexpr float kFar = 64.0f;
+constexpr float kMostTotal = 0x1p120f;  // a row's sum past this may have overflowed
 constexpr unsigned long long kDrainNs = 1000000000ull;  // bound on the wait for the MMAs in flight at the end
 
 // How a step's keys and values were written (by the decoding warps, for the others).  Where
@@ -145,6 +153,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_kv_plan(const __grid_constant_
   for (int i = 0; i < QLORA_KV_MAX_BATCH / kPlanThreads; ++i) {
     tiles[i] = 0;
     if (b0 + i < b1) {
+      a.again[b0 + i] = 0;
       const int rows = kv_seq(a.kb, b0 + i).n * a.group;
       if (rows > a.few_rows) tiles[i] = (rows + C::ROWS - 1) / C::ROWS;
     }
@@ -496,7 +505,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       tok0 = sg.lo + sg.step0 * N;
       }
 
-      float ref = kFloor, mx = kFloor, rv = kFloor, l = 0.0f;
+      float ref = kFloor, mx = kFloor, rv = kFloor, l = 0.0f, far = kFloor;
       for (int step = 0; step < nsteps; ++step, ++steps_done, ++all_steps, tok0 += N) {
         const int st = all_steps & 1;
         // The scores first: while this half sat out items, phases of cfull passed that it did not wait
@@ -633,7 +642,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
             renew(c, top, fmaxf(rv, top + e_c));
             plain(true, c, v, usual, sum);
           }
-          l = fmaf(sum, ex2(ref - e_c - mx), l);
+          const float unit = ref - e_c - mx;  // of the sum, in binades above the row's maximum
+          far = fmaxf(far, unit);
+          l = fmaf(sum, ex2(unit), l);
           const uint32_t to = p_tmem + c * 32;  // over the scores just read, or apart from them
           if (!vwide) {
             if constexpr (TW == 32) tmem_st16(to, reinterpret_cast<const uint32_t(&)[16]>(w));
@@ -662,6 +673,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       const int row = m * 128 + r, rr = sg.tile * C::ROWS + row;
       const bool live = row < sg.rows;
       const int tok = live ? rr / a.group : 0, h = live ? rr - tok * a.group : 0;
+      if (live && (far > kFar || l > kMostTotal)) a.again[sg.b] = 1;
       const bool any = l > 0.0f || l != l;
       const float half_unit = ex2(0.5f * (ref - mx));  // applied twice: it may pass float32's exponents
       const float inv = any ? a.v_unit / l * half_unit : 0.0f;

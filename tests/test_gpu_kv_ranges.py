@@ -88,3 +88,18 @@ def test_huge_value_far_below_the_highest_score(dim, n):
     t, values = _near(np.random.default_rng(31), 90), np.ones((90, dim // 64))
     t[40], values[40] = -150.0, 2.0 ** 123
     _run(t, values, n, 2, 4, dim, extra=2.0 ** (123 - 148))
+
+
+# ---------------------------------------------------------------- prompt chunks: several steps of one item
+# With 160 heads a worker does whole items; with one head every step has a worker of its own and the
+# parts are joined.
+@pytest.mark.parametrize("heads", [160, 1])
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("first,second", [(40, -100), (100, -50), (8, -126), (3, -120), (60, -80), (-100, 40), (-80, 60)])
+def test_steps_of_very_different_sizes(dim, first, second, heads):
+    """What tokens weigh in the softmax does not depend on the size of their values."""
+    rng, step = np.random.default_rng(32), _step(dim)
+    length = 2 * step + 37
+    size = np.full((length, dim // 64), 2.0 ** second)
+    size[:step] = 2.0 ** first
+    _run(_near(rng, length), size, 60, heads, 4, dim)

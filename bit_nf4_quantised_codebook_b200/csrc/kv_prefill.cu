@@ -19,7 +19,7 @@
 // The blocks' constants.  Where the constants of a step lie within a few binades of one
 // another (every step of ordinary data) they are multiplied into the fp16 levels, relative to
 // one exponent for the step's keys and one for its values.  Where they do not - a constant far
-// from the others, or not finite - the step is "wide": each token's keys have an exponent of
+// from the others, a value's that is zero, or one not finite - the step is "wide": each token's keys have an exponent of
 // their own that multiplies its scores, the values stay levels, and their constants multiply
 // the weights, one set of weights and one product per block of 64 channels.  So a value that a
 // row does not see can be of any size, or NaN, and leaves the row as it is.
@@ -813,7 +813,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
             const bool none = tile_of(i) >= TILES || lo + step * N + 16 * tile_of(i) + tok >= len;
             bits[i][k] = none ? 0 : c;
             most = max(most, bits[i][k]);
-            if (bits[i][k] != 0) least = min(least, bits[i][k]);
+            // (a value of zero is apart from all others: it contributes nothing, and folded in, with a high
+            // score, it would set the weights' reference)
+            if (keys ? bits[i][k] != 0 : !none) least = min(least, bits[i][k]);
           }
         if (step + 1 < nsteps) {
           fetch(step + 1, page, st ^ 1);
@@ -843,7 +845,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         // ---- constants: folded into the operands (keys below 2^12, values below 2), or apart
         auto exponent = [](uint32_t b) { return static_cast<int>(b >> 7) - 127; };
         const int e = most ? exponent(most) : 0;
-        const bool wide = most >= 0x7F80u || e < -100 || e > 110 || (most && e - exponent(least) > near);
+        const bool wide = most >= 0x7F80u || e < -100 || e > 110 || e - exponent(least) > near;  // (least 0xFFFF: none)
         __half2 hc[MINE][NB];
         if (!wide) {
           const float f = pow2(keys ? 11 - e : -e);

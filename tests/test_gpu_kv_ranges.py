@@ -103,3 +103,24 @@ def test_steps_of_very_different_sizes(dim, first, second, heads):
     size = np.full((length, dim // 64), 2.0 ** second)
     size[:step] = 2.0 ** first
     _run(_near(rng, length), size, 60, heads, 4, dim)
+
+
+@pytest.mark.parametrize("heads", [160, 1])
+@pytest.mark.parametrize("exponent", [-17, -30, -100])
+@pytest.mark.parametrize("at", [0, 1, 2])
+@pytest.mark.parametrize("dim", DIMS)
+def test_step_of_zero_values(dim, at, exponent, heads):
+    """A whole step of tokens without values, with the highest scores, before, between and after small values."""
+    rng, step = np.random.default_rng(33), _step(dim)
+    length = 3 * step + 20
+    t, size = _near(rng, length), np.full((length, dim // 64), 1.3125 * 2.0 ** exponent)
+    t[at * step:(at + 1) * step] += 8
+    size[at * step:(at + 1) * step] = 0.0
+    want, bound = _run(t, size, 60, heads, 4, dim)
+    assert (bound <= 0.02 * np.abs(want)).all()
+
+
+def test_values_of_nothing_but_zeros():
+    for n in (1, 60):
+        want, _ = _run(_near(np.random.default_rng(34), 300), np.zeros((300, 2)), n, 2, 4, 128)
+        assert not want.any()

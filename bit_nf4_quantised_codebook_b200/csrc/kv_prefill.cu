@@ -550,15 +550,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           sum = low(total0) + high(total0);
           return __low2float(most) > kMostWeight || __high2float(most) > kMostWeight;
         };
-        // The reference moves: to the largest score `top` and the largest contribution `big` so far.
-        // What was accumulated, and weighed in the passes of this step before this one, follows.
+        // The reference moves: to the largest score and the largest contribution so far, with `top` and
+        // `big` of this pass (an earlier step's score says nothing of contributions in this step's
+        // exponent).  What was accumulated, and weighed in the passes of this step before this one, follows.
         auto renew = [&](int c, float top, float big) {
-          rv = big;
+          rv = fmaxf(rv, big);
           const float next = ceilf(fmaxf(rv - kLift, top + e_c - 100.0f));
           const float f = next > ref ? ex2(ref - next) : 1.0f;  // a power of two
           ref = fmaxf(ref, next);
-          l *= ex2(mx - top);
-          mx = top;
+          const float highest = fmaxf(mx, top);
+          l *= ex2(mx - highest);
+          mx = highest;
           tmem_st_wait();
           auto rescale = [&](uint32_t from, int cols, auto scale) {
 #pragma unroll 1
@@ -586,7 +588,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         // (Three chunks, 1400 tokens together, took 176 us when masked steps went through it as well.)
         auto careful = [&](int c, const uint32_t (&v)[TW], uint32_t (&w)[NB * TW / 2], float &sum) {
           float s[TW];
-          float top = mx, big = rv;
+          float top = -INFINITY, big = -INFINITY;
 #pragma unroll
           for (int j = 0; j < TW; ++j) {
             const int t = tok0 + c * TW + j;
@@ -619,7 +621,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
 #pragma unroll
               for (int k = 0; k < NB; ++k) big = fmaxf(big, s[j] + lg2(cvr[k * N + c * TW + j]) + e_c);
             }
-            if (!vwide) big = fmaxf(big, top + e_c);
+            if (!vwide) big = top + e_c;
             renew(c, top, big);
           }
         };
@@ -638,8 +640,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
 #pragma unroll
             for (int j = 0; j < TW; ++j)
               if (!hide || seen(c, j)) most = fmaxf(most, __uint_as_float(v[j]));
-            const float top = fmaxf(mx, most * factor);
-            renew(c, top, fmaxf(rv, top + e_c));
+            most *= factor;
+            renew(c, most, most + e_c);
             plain(true, c, v, usual, sum);
           }
           const float unit = ref - e_c - mx;  // of the sum, in binades above the row's maximum

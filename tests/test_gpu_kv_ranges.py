@@ -124,3 +124,21 @@ def test_values_of_nothing_but_zeros():
     for n in (1, 60):
         want, _ = _run(_near(np.random.default_rng(34), 300), np.zeros((300, 2)), n, 2, 4, 128)
         assert not want.any()
+
+
+@pytest.mark.parametrize("far", [0, 1])
+@pytest.mark.parametrize("dim", DIMS)
+def test_highest_score_of_small_values_before_larger_contributions(dim, far):
+    """The first step has the highest scores and the smallest values, the second contributes 2^8 times as
+    much; with `far` one key of the second is 2^-14 of the others (its constants are apart)."""
+    rng, step = np.random.default_rng(35), _step(dim)
+    length = 2 * step
+    size = np.full((length, dim // 64), 1.3125 * 2.0 ** 20)
+    t = np.round(rng.uniform(-1.5, 1.5, length) * 2) / 2  # (eight bits of significand, with what is added)
+    t[step:] += 30
+    if far:
+        t[step + 3] = 2.0 ** -10
+    t[:step] += 100
+    size[:step] = 2.0 ** -60
+    want, bound = _run(t, size, 60, 160, 4, dim)
+    assert (bound <= 0.02 * np.abs(want)).all()

@@ -31,7 +31,10 @@
 // The weights carry their step's exponent, and so does their sum, which is brought to the
 // row's maximum before it is added: where a step's values are so small beside what the row has
 // seen that the sum would lose terms (kFar), the sequence is marked in `again`, and the few-row kernel,
-// launched behind this one, whose sums know nothing of the values, computes it anew.
+// launched behind this one, whose sums know nothing of the values, computes it anew.  So is one where a
+// block's largest contribution to a row weighs less than 2^kLeast, because another block's or a token
+// whose values are zero set the row's only reference: the few-row kernel has one per block.  (Marked
+// for one block of 2^31, 4096 over 8192 takes 4.4 ms in place of 0.57.)
 //
 // Measured (4096 tokens x 4 query heads over 8192 cached, 8 key/value heads of 128): 0.56 ms,
 // 742 TFLOP/s of the visible pairs.  A step takes 5200 clocks, of which the tensor cores work
@@ -76,7 +79,7 @@ struct PreCfg {
   static constexpr int BARS = 19;
   static constexpr int MISC_FLOATS = 2 * N + 2 * NB * N;
   static constexpr int MISC_BYTES = MISC_FLOATS * 4 + 4 * 8 + 2 * 7 * 8 + BARS * 8 + 48;
-  static constexpr int SMEM_BYTES = 0x20000 + KV_BYTES + MT * Q_BYTES;
+  static constexpr int SMEM_BYTES = 0x20000 + KV_BYTES + MT * Q_BYTES + ROWS * NB * 4;
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory of one CTA");
   static_assert(O_COL + MT * D <= TMEM_COLS, "TMEM columns");
 };
@@ -91,6 +94,9 @@ constexpr int kItemOverhead = 2;  // three chunks, 1400 tokens together: 152, 14
 // lost is 2^-62 of that weight or less.  Ordinary steps stay below 10.
 constexpr float kFar = 64.0f;
 constexpr float kMostTotal = 0x1p120f;  // a row's sum past this may have overflowed
+// A block's largest contribution must weigh at least 2^kLeast: what vanishes beside it is then 2^-23 of it.
+constexpr float kLeast = -2.0f;
+constexpr float kSeen = -1.0e38f;  // a contribution of unknown size
 constexpr unsigned long long kDrainNs = 1000000000ull;  // bound on the wait for the MMAs in flight at the end
 
 // How a step's keys and values were written (by the decoding warps, for the others).  Where
@@ -330,9 +336,11 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
   const uint32_t smem_base = smem_u32(smem);
   const uint32_t table = (smem_base + 0xFFFFu) & ~0xFFFFu;  // 64 KiB at a multiple of 64 KiB
   // before the table: keys, constants, barriers; in its gaps (the upper half of each 256
-  // bytes): two stages of codes; after it: values and queries
+  // bytes): two stages of codes; after it: values, queries and [NB][ROWS] each row's largest
+  // contribution to each block in wide steps, as a logarithm
   const uint32_t k_smem = (smem_base + 1023u) & ~1023u;
   const uint32_t v_smem = table + 0x10000u, q_smem = v_smem + C::KV_BYTES;
+  float *largest = reinterpret_cast<float *>(smem + (q_smem - smem_base) + MT * C::Q_BYTES);
   float *cs = reinterpret_cast<float *>(smem + (k_smem - smem_base) + C::KV_BYTES);  // [2][N] score factors
   float *cv = cs + 2 * N;                                                            // [2][NB][N] value constants
   StepInfo *kinfo = reinterpret_cast<StepInfo *>(cv + 2 * NB * N), *vinfo = kinfo + 2;  // [2] each
@@ -506,6 +514,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       }
 
       float ref = kFloor, mx = kFloor, rv = kFloor, l = 0.0f, far = kFloor;
+      float folded = kFloor;  // largest contribution in steps that are not wide, when last renewed
+      bool apart = false;     // there was a wide step
       for (int step = 0; step < nsteps; ++step, ++steps_done, ++all_steps, tok0 += N) {
         const int st = all_steps & 1;
         // The scores first: while this half sat out items, phases of cfull passed that it did not wait
@@ -523,6 +533,15 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         const float e_c = hv.scale;
         const float *csr = cs + st * N, *cvr = cv + st * NB * N;
         const float factor = hk.scale * qs;
+        auto unit_of_sums = [&] { return ref - e_c - mx; };  // in binades above the row's maximum
+        far = fmaxf(far, unit_of_sums());
+        if (!vwide) {
+          if (tok0 < see_hi && tok0 + N > see_lo) folded = fmaxf(folded, kSeen);
+        } else if (!apart) {
+          apart = true;
+#pragma unroll
+          for (int k = 0; k < NB; ++k) largest[k * C::ROWS + m * 128 + r] = kFloor;
+        }
         // The usual pass over TW columns: v holds their products, w receives the weights; two
         // columns per instruction where there is a paired one.  With `masked` the columns that the row
         // does not see weigh nothing (their constants, folded into the operands, are finite).
@@ -555,12 +574,14 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         // exponent).  What was accumulated, and weighed in the passes of this step before this one, follows.
         auto renew = [&](int c, float top, float big) {
           rv = fmaxf(rv, big);
+          if (!vwide) folded = fmaxf(folded, big);
           const float next = ceilf(fmaxf(rv - kLift, top + e_c - 100.0f));
           const float f = next > ref ? ex2(ref - next) : 1.0f;  // a power of two
           ref = fmaxf(ref, next);
           const float highest = fmaxf(mx, top);
           l *= ex2(mx - highest);
           mx = highest;
+          far = fmaxf(far, unit_of_sums());
           tmem_st_wait();
           auto rescale = [&](uint32_t from, int cols, auto scale) {
 #pragma unroll 1
@@ -589,6 +610,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         auto careful = [&](int c, const uint32_t (&v)[TW], uint32_t (&w)[NB * TW / 2], float &sum) {
           float s[TW];
           float top = -INFINITY, big = -INFINITY;
+          float block_most[NB];
 #pragma unroll
           for (int j = 0; j < TW; ++j) {
             const int t = tok0 + c * TW + j;
@@ -597,8 +619,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           }
 #pragma unroll 1
           for (int pass = 0; pass < 2; ++pass) {
-            float most = 0.0f;
             sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < NB; ++k) block_most[k] = 0.0f;
 #pragma unroll
             for (int j = 0; j < TW; j += 2) {
               const float p0 = ex2(s[j] - (ref - e_c)), p1 = ex2(s[j + 1] - (ref - e_c));
@@ -607,12 +630,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
               for (int k = 0; k < NB; ++k) {
                 if (k > 0 && !vwide) continue;
                 const float c0 = vwide ? cvr[k * N + c * TW + j] : 1.0f, c1 = vwide ? cvr[k * N + c * TW + j + 1] : 1.0f;
-                // a token that a row does not see adds nothing, whatever its value's constant
-                const float w0 = s[j] == -INFINITY ? 0.0f : p0 * c0, w1 = s[j + 1] == -INFINITY ? 0.0f : p1 * c1;
-                most = fmaxf(most, fmaxf(w0, w1));
+                // a token that a row does not see adds nothing, whatever its value's constant; one that it
+                // sees is zero in block_most only if the constant is
+                const float w0 = s[j] == -INFINITY ? 0.0f : (p0 + 0x1p-120f) * c0,
+                            w1 = s[j + 1] == -INFINITY ? 0.0f : (p1 + 0x1p-120f) * c1;
+                block_most[k] = fmaxf(block_most[k], fmaxf(w0, w1));
                 w[k * (TW / 2) + j / 2] = pack_half2(w0, w1);
               }
             }
+            float most = block_most[0];
+#pragma unroll
+            for (int k = 1; k < NB; ++k) most = fmaxf(most, block_most[k]);
             if (pass == 1 || !__any_sync(0xFFFFFFFFu, most > kMostWeight || sum > kMostSum)) break;
 #pragma unroll
             for (int j = 0; j < TW; ++j) {
@@ -623,6 +651,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
             }
             if (!vwide) big = top + e_c;
             renew(c, top, big);
+          }
+          if (vwide) {
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+              float &mine = largest[k * C::ROWS + m * 128 + r];
+              mine = fmaxf(mine, ref + lg2(block_most[k]));
+            }
           }
         };
 #pragma unroll 1
@@ -644,9 +679,7 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
             renew(c, most, most + e_c);
             plain(true, c, v, usual, sum);
           }
-          const float unit = ref - e_c - mx;  // of the sum, in binades above the row's maximum
-          far = fmaxf(far, unit);
-          l = fmaf(sum, ex2(unit), l);
+          l = fmaf(sum, ex2(unit_of_sums()), l);
           const uint32_t to = p_tmem + c * 32;  // over the scores just read, or apart from them
           if (!vwide) {
             if constexpr (TW == 32) tmem_st16(to, reinterpret_cast<const uint32_t(&)[16]>(w));
@@ -675,7 +708,17 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
       const int row = m * 128 + r, rr = sg.tile * C::ROWS + row;
       const bool live = row < sg.rows;
       const int tok = live ? rr / a.group : 0, h = live ? rr - tok * a.group : 0;
-      if (live && (far > kFar || l > kMostTotal)) a.again[sg.b] = 1;
+      bool lost = far > kFar || l > kMostTotal;
+      if (apart && l > 0.0f) {
+        // What a step that is not wide contributes reaches every block, within 2^kNearValues; it is enough where the
+        // reference is its own (the largest then weighs 2^(kLift - 1) or more).
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          const float top = fmaxf(largest[k * C::ROWS + row], folded - (kLift - 1.0f - kLeast));
+          lost |= top > kFloor && top - ref < kLeast;
+        }
+      }
+      if (live && lost) a.again[sg.b] = 1;
       const bool any = l > 0.0f || l != l;
       const float half_unit = ex2(0.5f * (ref - mx));  // applied twice: it may pass float32's exponents
       const float inv = any ? a.v_unit / l * half_unit : 0.0f;
@@ -805,7 +848,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         const int st = n & 1;
         // ---- the range of the step's constants
         uint32_t bits[MINE][NB];
+        // least: without keys of zero (they wrap past all others); 0xFFFF where there is none
         uint32_t most = 0, least = 0xFFFFu;
+        const uint32_t wrap = keys ? 1u : 0u;
 #pragma unroll
         for (int i = 0; i < MINE; ++i)
 #pragma unroll
@@ -815,9 +860,9 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
             const bool none = tile_of(i) >= TILES || lo + step * N + 16 * tile_of(i) + tok >= len;
             bits[i][k] = none ? 0 : c;
             most = max(most, bits[i][k]);
-            // (a value of zero is apart from all others: it contributes nothing, and folded in, with a high
+            // (a value of zero is far from all others: it contributes nothing, and folded in, with a high
             // score, it would set the weights' reference)
-            if (keys ? bits[i][k] != 0 : !none) least = min(least, bits[i][k]);
+            least = min(least, none ? 0xFFFFu : c - wrap);
           }
         if (step + 1 < nsteps) {
           fetch(step + 1, page, st ^ 1);
@@ -847,7 +892,8 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
         // ---- constants: folded into the operands (keys below 2^12, values below 2), or apart
         auto exponent = [](uint32_t b) { return static_cast<int>(b >> 7) - 127; };
         const int e = most ? exponent(most) : 0;
-        const bool wide = most >= 0x7F80u || e < -100 || e > 110 || e - exponent(least) > near;  // (least 0xFFFF: none)
+        const bool wide = most >= 0x7F80u || e < -100 || e > 110 ||
+                          (least != 0xFFFFu && e - exponent(least + wrap) > near);
         __half2 hc[MINE][NB];
         if (!wide) {
           const float f = pow2(keys ? 11 - e : -e);

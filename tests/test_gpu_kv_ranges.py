@@ -142,3 +142,111 @@ def test_highest_score_of_small_values_before_larger_contributions(dim, far):
     size[:step] = 2.0 ** -60
     want, bound = _run(t, size, 60, 160, 4, dim)
     assert (bound <= 0.02 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("heads", [160, 1])
+@pytest.mark.parametrize("above", [12, 30, 60, 110, 120, 250])
+@pytest.mark.parametrize("dim", DIMS)
+def test_token_without_values_above_all_others(dim, above, heads):
+    """One token of a step has zero values and takes nearly all the weight: what the others contribute keeps
+    its precision."""
+    rng, step = np.random.default_rng(36), _step(dim)
+    length = 2 * step + 11
+    t, size = _near(rng, length), np.full((length, dim // 64), 1.3125)
+    t[step + 5], size[step + 5] = above, 0.0
+    want, bound = _run(t, size, 60, heads, 4, dim)
+    assert above == 250 or (bound <= 0.05 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("heads", [160, 1])
+@pytest.mark.parametrize("at", [0, 1, 2])
+@pytest.mark.parametrize("larger", [10, 20, 31, 70])
+@pytest.mark.parametrize("dim", [128, 256])
+def test_blocks_of_very_different_sizes(dim, larger, at, heads):
+    """In one step the first 64 channels' values are 2^larger times the others'; each block keeps its precision."""
+    rng, step = np.random.default_rng(37), _step(dim)
+    length = 3 * step
+    t, size = _near(rng, length), np.full((length, dim // 64), 1.3125)
+    size[at * step:(at + 1) * step, 0] *= 2.0 ** larger
+    want, bound = _run(t, size, 60, heads, 4, dim)
+    assert (bound <= 0.02 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("dim", [128, 256])
+def test_blocks_that_every_step_has_far_apart(dim):
+    """A block 2^40 smaller throughout, and one of zeros."""
+    rng = np.random.default_rng(38)
+    for small in (2.0 ** -40, 0.0):
+        length = 2 * _step(dim) + 50
+        size = np.full((length, dim // 64), 1.3125)
+        size[:, -1] = 1.3125 * small
+        _run(_near(rng, length), size, 60, 160, 4, dim)
+
+
+def _weird_and_ordinary(a, dim=128, heads=2, n=60):
+    """Two sequences of three steps, the first with blocks far apart, and a single token over the second; the
+    caches' values and the expected outputs' ingredients."""
+    rng, step = np.random.default_rng(39), _step(dim)
+    length = 3 * step
+    signs = np.where(rng.random(dim) < 0.5, -1.0, 1.0)
+    case = Case([n, n, 1], [length, length, length], page_size=16, seed=31)
+    case.table[2] = case.table[1]
+    both = []
+    c = None
+    for b in range(2):
+        t, size = _near(rng, length), np.full((length, dim // 64), 1.3125)
+        if b == 0:
+            size[:step, 0] *= 2.0 ** 31
+        one = Case([length], [length], page_size=16)
+        one.num_pages, one.table = case.num_pages, case.table[b:b + 1]
+        filled, K, V = _fill(a, t, size, heads, dim, signs, one)
+        if c is None:
+            c = filled
+        else:
+            pages = torch.from_numpy(one.table[0].astype(np.int64)).cuda()
+            for name in ("k_codes", "k_absmax", "v_codes", "v_absmax"):
+                getattr(c, name)[pages] = getattr(filled, name)[pages]
+        both.append((K, V))
+    return case, c, both, signs
+
+
+def test_other_sequences_of_the_call_keep_their_bits():
+    """A sequence whose blocks lie far apart beside an ordinary one, which comes out as it does alone; and
+    in a graph, whose replays follow what the cache holds."""
+    a = api()
+    dim, heads, group, n = 128, 2, 4, 60
+    case, c, both, _ = _weird_and_ordinary(a)
+    batch = case.batch(a)
+    Q = torch.ones(case.tokens, heads * group, dim, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(Q, 7.0)
+    err = a.new_error_word()
+    ws = torch.empty(a.qlora_kv_attention_workspace_size(c, 3, case.tokens, heads * group), dtype=torch.uint8, device="cuda")
+    attend = lambda: a.qlora_kv_attention(c, batch, Q, scale=_scale(dim), causal=False, out=out, ws=ws, dev_err=err)
+
+    def check(first):
+        torch.cuda.synchronize()
+        check_dev_err(err)
+        for rows, which in ((slice(0, n), first), (slice(n, 2 * n + 1), 1)):
+            off, _, _ = _off(out[rows], *both[which], dim)
+            assert off <= 0, off
+
+    attend()
+    check(0)
+    direct = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        attend()
+    ws.fill_(0xFF)
+    out.fill_(7.0)
+    graph.replay()
+    check(0)
+    assert torch.equal(out.view(torch.int16), direct.view(torch.int16))
+    batch.page_table[0] = batch.page_table[1]  # the first sequence becomes an ordinary one
+    graph.replay()
+    check(1)
+    assert torch.equal(out[n:].view(torch.int16), direct[n:].view(torch.int16))
+    assert torch.equal(out[:n].view(torch.int16), direct[n:2 * n].view(torch.int16))
+    batch.page_table.copy_(torch.from_numpy(case.table))
+    graph.replay()
+    check(0)
+    assert torch.equal(out.view(torch.int16), direct.view(torch.int16))

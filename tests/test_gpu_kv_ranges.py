@@ -250,3 +250,17 @@ def test_other_sequences_of_the_call_keep_their_bits():
     graph.replay()
     check(0)
     assert torch.equal(out.view(torch.int16), direct.view(torch.int16))
+
+
+@pytest.mark.parametrize("n", [1, 2, 60])
+@pytest.mark.parametrize("dim", DIMS)
+def test_peaked_softmax(dim, n):
+    """Scores of 0 to 250 binades in no order, so that references move again and again, by little and
+    by much; the outputs are told from those of any other order of weights."""
+    rng = np.random.default_rng(40)
+    for top in (20, 60, 250):
+        length = 3 * _step(dim) + 7
+        t = np.round(rng.uniform(0, top, length))
+        size = rng.choice([0.5, 1.0, 1.3125, 3.0], (length, dim // 64))
+        want, bound = _run(t, size, n, 3, 4, dim)
+        assert (bound <= 0.1 * np.abs(want)).all()

@@ -446,6 +446,12 @@ def _kv_stream(device: int) -> int:
     return torch._C._cuda_getCurrentRawStream(device)
 
 
+def _int(x: int) -> int:
+    """x as a C int takes it, what it does not hold as -1 or its largest value (a conversion would drop the
+    upper bits)."""
+    return max(-1, min(x, 0x7FFFFFFF))
+
+
 @dataclass(frozen=True, eq=False)
 class KVCache:
     """A paged cache of keys and values in 4 bits (qlora_kv_cache of the C header).
@@ -587,7 +593,7 @@ def qlora_kv_read(cache: KVCache, batch: KVBatch, tokens: int, K_out: torch.Tens
 
 def qlora_kv_attention_workspace_size(cache: KVCache, batch: int, tokens: int, q_heads: int) -> int:
     n = ctypes.c_size_t()
-    _check(lib().qlora_kv_attention_workspace_size(cache._c, batch, tokens, q_heads, ctypes.byref(n)),
+    _check(lib().qlora_kv_attention_workspace_size(cache._c, _int(batch), tokens, _int(q_heads), ctypes.byref(n)),
            "qlora_kv_attention_workspace_size")
     return n.value
 
@@ -614,7 +620,7 @@ def qlora_kv_attention(cache: KVCache, batch: KVBatch, Q: torch.Tensor, scale: f
     if tokens == 0:
         return out
     st = lib().qlora_kv_attention(cache._c, batch.c_struct(tokens), Q.data_ptr(), q_heads, qt, qh,
-                                  dim ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
+                                  dim ** -0.5 if scale is None else scale, bool(causal), _int(window), out.data_ptr(),
                                   ws.data_ptr(), ws.nbytes, _ptr(dev_err), stream)
     if st:
         _check(st, "qlora_kv_attention")

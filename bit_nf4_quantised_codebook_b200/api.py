@@ -539,6 +539,14 @@ def _kv_devices(cache: KVCache, batch: KVBatch, *tensors) -> None:
             raise QloraError(f"a tensor of shape {tuple(t.shape)} is on {t.device}, the cache on cuda:{d}")
 
 
+def _kv_error_word(dev_err: torch.Tensor | None) -> int | None:
+    if dev_err is None:
+        return None
+    if dev_err.dtype != torch.int32 or dev_err.numel() == 0:
+        raise QloraError(f"dev_err: expected int32 with an element or more, got {dev_err.dtype} {tuple(dev_err.shape)}")
+    return dev_err.data_ptr()
+
+
 def _kv_rows(t: torch.Tensor, heads, head_dim: int, name: str) -> tuple[int, int]:
     """A bfloat16 [tokens, heads, head_dim] tensor whose channels are contiguous (rows and heads may be
     strided); returns its row and head strides (0 for an axis of one element)."""
@@ -563,7 +571,7 @@ def qlora_kv_append(cache: KVCache, batch: KVBatch, K: torch.Tensor, V: torch.Te
     if K.shape[0] == 0:
         return
     st = lib().qlora_kv_append(cache._c, batch.c_struct(K.shape[0]), K.data_ptr(), kt, kh, V.data_ptr(), vt, vh,
-                               _ptr(dev_err), stream)
+                               _kv_error_word(dev_err), stream)
     if st:
         _check(st, "qlora_kv_append")
 
@@ -585,7 +593,8 @@ def qlora_kv_read(cache: KVCache, batch: KVBatch, tokens: int, K_out: torch.Tens
     stream = _kv_stream(cache._device)
     if tokens == 0:
         return K_out, V_out
-    st = lib().qlora_kv_read(cache._c, batch.c_struct(tokens), _ptr(K_out), _ptr(V_out), _ptr(dev_err), stream)
+    st = lib().qlora_kv_read(cache._c, batch.c_struct(tokens), _ptr(K_out), _ptr(V_out), _kv_error_word(dev_err),
+                             stream)
     if st:
         _check(st, "qlora_kv_read")
     return K_out, V_out
@@ -615,13 +624,15 @@ def qlora_kv_attention(cache: KVCache, batch: KVBatch, Q: torch.Tensor, scale: f
     if ws is None:
         need = qlora_kv_attention_workspace_size(cache, batch.batch, tokens, q_heads)
         ws = torch.empty(max(need, 16), dtype=torch.uint8, device=Q.device)
+    elif not ws.is_contiguous():
+        raise QloraError(f"ws: expected a contiguous tensor, got {tuple(ws.shape)} strides {ws.stride()}")
     _kv_devices(cache, batch, Q, out, ws, dev_err)
     stream = _kv_stream(cache._device)
     if tokens == 0:
         return out
     st = lib().qlora_kv_attention(cache._c, batch.c_struct(tokens), Q.data_ptr(), q_heads, qt, qh,
                                   dim ** -0.5 if scale is None else scale, bool(causal), _int(window), out.data_ptr(),
-                                  ws.data_ptr(), ws.nbytes, _ptr(dev_err), stream)
+                                  ws.data_ptr(), ws.nbytes, _kv_error_word(dev_err), stream)
     if st:
         _check(st, "qlora_kv_attention")
     return out

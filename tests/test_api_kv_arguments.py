@@ -61,3 +61,38 @@ def test_workspace_of_sizes_past_an_int_is_refused():
     for batch, q_heads in ((2 ** 32 + 1, 4), (1, 2 ** 32 + 4), (1 - 2 ** 32, 4)):
         with pytest.raises(api.QloraError):
             api.qlora_kv_attention_workspace_size(cache, batch, 1, q_heads)
+
+
+def _error_words():
+    whole = torch.zeros(8, dtype=torch.uint8)
+    return [torch.zeros(4, dtype=torch.int64), whole[1:5], torch.zeros(0, dtype=torch.int32),
+            torch.zeros(4, dtype=torch.float32)]
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_error_word_of_another_type_is_refused(kv, monkeypatch, which):
+    """Kernels add bits to one int32: anything else would be written beside, or at no multiple of four bytes."""
+    monkeypatch.setattr(kv.api, "_need", lambda *a: None)
+    wrong, api = _error_words()[which], kv.api
+    K = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    for call in (lambda: api.qlora_kv_append(kv.cache, kv.batch, K, K, dev_err=wrong),
+                 lambda: api.qlora_kv_read(kv.cache, kv.batch, 3, K_out=K, dev_err=wrong),
+                 lambda: api.qlora_kv_attention(kv.cache, kv.batch, kv.Q, out=kv.out, ws=kv.ws, dev_err=wrong)):
+        with pytest.raises(api.QloraError, match="dev_err"):
+            call()
+    assert kv.library.calls == []
+
+
+def test_workspace_without_memory_of_its_own_is_refused(kv, monkeypatch):
+    """An expanded or strided tensor counts bytes that it does not have side by side."""
+    monkeypatch.setattr(kv.api, "_need", lambda *a: None)
+    for wrong in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), kv.ws[::2]):
+        with pytest.raises(kv.api.QloraError, match="ws"):
+            kv.api.qlora_kv_attention(kv.cache, kv.batch, kv.Q, out=kv.out, ws=wrong)
+    assert kv.library.calls == []
+
+
+def test_sound_scratch_passes(kv, monkeypatch):
+    word = torch.zeros(4, dtype=torch.int32)
+    args = _attention_args(kv, monkeypatch, dev_err=word)
+    assert (args["dev_err"], args["ws"], args["ws_bytes"]) == (word.data_ptr(), kv.ws.data_ptr(), 4096)

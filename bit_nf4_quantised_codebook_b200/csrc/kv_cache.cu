@@ -104,6 +104,15 @@ __device__ __forceinline__ uint32_t token_row(const KvBatch &kb, int heads, int 
   return ((static_cast<uint32_t>(page) * heads) << kb.page_shift) + (p & ((1 << kb.page_shift) - 1));
 }
 
+// The CTAs behind the last token row, launched where there is an error word: the first checks every
+// sequence, those too that no row leads to (beside the others: a step of 16 tokens takes as long as without).
+__device__ __forceinline__ bool checks_batch(const KvBatch &kb, int t0) {
+  if (t0 < kb.tokens) return false;
+  if (blockIdx.y == 0)
+    for (int b = threadIdx.x; b < kb.batch; b += kKvThreads) kv_seq(kb, b);
+  return true;
+}
+
 // The cache rows of this CTA's tokens, into shared memory; returns how many tokens.
 __device__ __forceinline__ int load_rows(const KvBatch &kb, const KvRows &r, int t0, uint32_t *rows) {
   const int n = min(r.tokens_per_cta, kb.tokens - t0);
@@ -187,6 +196,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_append(const __grid_constant_
   pdl_wait();
   pdl_launch_dependents();
   const int t0 = static_cast<int>(blockIdx.x) * r.tokens_per_cta;
+  if (checks_batch(kb, t0)) return;
   const int n = load_rows(kb, r, t0, s_row);
   uint4 raw[UNITS][2];
   uint32_t row[UNITS], sub[UNITS];
@@ -234,6 +244,7 @@ __global__ void __launch_bounds__(kKvThreads) k_kv_read(const __grid_constant__ 
   pdl_wait();
   pdl_launch_dependents();
   const int t0 = static_cast<int>(blockIdx.x) * r.tokens_per_cta;
+  if (checks_batch(kb, t0)) return;
   const int n = load_rows(kb, r, t0, s_row);
   uint32_t codes[UNITS][2], amax[UNITS][2];
   int64_t dst[UNITS];  // unit of the outputs, or -1
@@ -292,8 +303,9 @@ KvRows cache_rows(const qlora_kv_cache &c, int units) {
   return r;
 }
 
-dim3 rows_grid(const KvRows &r, int64_t tokens) {
-  return dim3(static_cast<unsigned>((tokens + r.tokens_per_cta - 1) / r.tokens_per_cta),
+dim3 rows_grid(const KvRows &r, const KvBatch &kb) {
+  return dim3(static_cast<unsigned>((static_cast<int64_t>(kb.tokens) + r.tokens_per_cta - 1) / r.tokens_per_cta) +
+                  (kb.dev_err ? 1u : 0u),
               static_cast<unsigned>((r.per_token + r.span - 1) / r.span));
 }
 
@@ -408,7 +420,7 @@ cudaError_t launch_kv_append(const qlora_kv_cache &c, const KvBatch &kb, const u
   r.head_stride[1] = v_head_stride;
   KvCodeTable t;
   std::memcpy(t.e, table, sizeof(t.e));
-  const dim3 grid = rows_grid(r, kb.tokens);
+  const dim3 grid = rows_grid(r, kb);
   auto go = [&](auto kern1, auto kern2) {
     return units == 1 ? launch_k(kern1, grid, dim3(kKvThreads), 0, st, 1, kb, r, t)
                       : launch_k(kern2, grid, dim3(kKvThreads), 0, st, 1, kb, r, t);
@@ -428,7 +440,7 @@ cudaError_t launch_kv_read(const qlora_kv_cache &c, const KvBatch &kb, uint16_t 
   r.dst[1] = V_out;
   Nf4Levels lv;
   std::memcpy(lv.q, levels, sizeof(lv.q));
-  const dim3 grid = rows_grid(r, kb.tokens);
+  const dim3 grid = rows_grid(r, kb);
   auto go = [&](auto kern1, auto kern2) {
     return units == 1 ? launch_k(kern1, grid, dim3(kKvThreads), 0, st, 1, kb, r, lv)
                       : launch_k(kern2, grid, dim3(kKvThreads), 0, st, 1, kb, r, lv);

@@ -33,8 +33,9 @@
 // seen that the sum would lose terms (kFar), the sequence is marked in `again`, and the few-row kernel,
 // launched behind this one, whose sums know nothing of the values, computes it anew.  So is one where a
 // block's largest contribution to a row weighs less than 2^kLeast, because another block's or a token
-// whose values are zero set the row's only reference: the few-row kernel has one per block.  (Marked
-// for one block of 2^31, 4096 over 8192 takes 4.4 ms in place of 0.57.)
+// whose values are zero set the row's only reference: the few-row kernel has one per block.  And so is one with
+// a key whose blocks lie more than 2^kNearBlocks apart: there, constants multiply float32 sums.  (Marked for
+// one block of 2^31, 4096 over 8192 takes 4.4 ms in place of 0.57.)
 //
 // Measured (4096 tokens x 4 query heads over 8192 cached, 8 key/value heads of 128): 0.56 ms,
 // 742 TFLOP/s of the visible pairs.  A step takes 5200 clocks, of which the tensor cores work
@@ -88,6 +89,9 @@ struct PreCfg {
 // into the fp16 operands: keys keep all their bits (fp16 has 25 binades below 2^12), and a
 // weight that vanishes in fp16 (2^-31 of the largest) can have a value 2^8 times another's.
 constexpr int kNearKeys = 12, kNearValues = 8;
+// Binades between the blocks of one key up to which the smaller ones keep their bits in fp16 (the largest is
+// held below 2^12, levels are 2^-7 of it or more).
+constexpr int kNearBlocks = 16;
 // What starting and ending an item costs a CTA, in steps: part of its place on the line.
 constexpr int kItemOverhead = 2;  // three chunks, 1400 tokens together: 152, 146, 148, 146 us with 1, 2, 3, 4
 // Binades between the unit of a step's sum and the row's largest weight: of 126 in float32, so that what is
@@ -795,11 +799,12 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
     uint32_t n = 0;  // steps of the CTA so far
     bool ok = true;
     while (ok) {
-      int lo, nsteps, head, len;
+      int b, lo, nsteps, head, len;
       const int32_t *pages;
       {
         Segment sg;
         if (!next_part<C>(p, my_line, entry, done_steps, sg)) break;
+        b = sg.b;
         nsteps = sg.step1 - sg.step0;
         lo = sg.lo + sg.step0 * N;
         head = sg.head;
@@ -909,9 +914,13 @@ __global__ void __launch_bounds__(C::THREADS, 1) k_kv_prefill(const __grid_const
           // each token's keys relative to their own exponent
 #pragma unroll
           for (int i = 0; i < MINE; ++i) {
-            uint32_t top = 0;
+            uint32_t top = 0, low = 0xFFFFu;
 #pragma unroll
-            for (int k = 0; k < NB; ++k) top = max(top, bits[i][k]);
+            for (int k = 0; k < NB; ++k) {
+              top = max(top, bits[i][k]);
+              if (bits[i][k] != 0) low = min(low, bits[i][k]);
+            }
+            if (NB > 1 && top < 0x7F80u && exponent(top) - exponent(low) > kNearBlocks) a.again[b] = 1;
             const int te = max(exponent(top), -110);
             const bool bad = top >= 0x7F80u;
 #pragma unroll

@@ -264,3 +264,29 @@ def test_peaked_softmax(dim, n):
         size = rng.choice([0.5, 1.0, 1.3125, 3.0], (length, dim // 64))
         want, bound = _run(t, size, n, 3, 4, dim)
         assert (bound <= 0.1 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("n", [1, 2, 60])
+@pytest.mark.parametrize("larger", [10, 20, 36, 40, 100])
+@pytest.mark.parametrize("dim", [128, 256])
+def test_key_blocks_of_very_different_sizes(dim, larger, n):
+    """The first 64 channels of some keys are 2^larger times the others, and the queries zero there: the scores
+    come from the small blocks alone."""
+    a = api()
+    rng, step, heads, group = np.random.default_rng(41), _step(dim), 3, 4
+    length = 2 * step + 9
+    t, signs = _near(rng, length, 5.0), np.where(rng.random(dim) < 0.5, -1.0, 1.0)
+    case = Case([n], [length], page_size=16, seed=32)
+    c, K, V = _fill(a, t, np.full((length, dim // 64), 1.3125), heads, dim, signs, case)
+    V = V * rng.choice([0.5, 1.0, 3.0], (length, 1, 1))  # (values that differ, so that the weights show)
+    K[::3, :, :64] = 2.0 ** larger
+    whole = Case([length], [length], page_size=16)
+    whole.table = case.table
+    a.qlora_kv_append(c, whole.batch(a), *(bf16(x).cuda().expand(-1, heads, -1) for x in (K, V)))
+    q = np.ones((1, 1, dim))
+    q[..., :64] = 0.0
+    out = a.qlora_kv_attention(c, case.batch(a), bf16(q).cuda().expand(n, heads * group, -1), scale=_scale(dim), causal=False)
+    want, bound = kv.attention(q, K, V, _scale(dim), False, 0, False)
+    assert (bound <= 0.02 * np.abs(want)).all()
+    off = (np.abs(f64(out) - want) - bound).max()
+    assert off <= 0, off

@@ -600,6 +600,8 @@ qlora_status qlora_kv_read(const qlora_kv_cache *cache, const qlora_kv_batch *ba
   if (st != QLORA_OK) return st;
   if (!K_out && !V_out) return QLORA_ERR_INVALID_ARG;
   if ((K_out && !aligned16(K_out)) || (V_out && !aligned16(V_out))) return QLORA_ERR_MISALIGNED;
+  const size_t out_bytes = static_cast<size_t>(batch->tokens) * cache->heads * cache->head_dim * 2;
+  if (K_out && V_out && overlap(K_out, out_bytes, V_out, out_bytes)) return QLORA_ERR_INVALID_ARG;
   if (!device_ok()) return QLORA_ERR_NO_DEVICE;
   if (batch->tokens == 0) return QLORA_OK;
   float levels[16];

@@ -447,7 +447,7 @@ qlora_status qlora_kv_append(const qlora_kv_cache *cache, const qlora_kv_batch *
  * qlora_kv_read — the stored keys and values of the same rows, dequantised:
  * x_hat = bf16_rn(float32(level[code] * absmax)).  With n_b = kv_len[b] a whole
  * sequence is read back.  K_out, V_out (each nullable): device bfloat16
- * [tokens][heads][head_dim], 16-byte aligned.  Rows whose position is negative
+ * [tokens][heads][head_dim], 16-byte aligned, not overlapping.  Rows whose position is negative
  * are left as they were and set QLORA_DEVERR_KV_INDEX.
  */
 qlora_status qlora_kv_read(const qlora_kv_cache *cache, const qlora_kv_batch *batch, uint16_t *K_out,

@@ -96,3 +96,19 @@ def test_sound_scratch_passes(kv, monkeypatch):
     word = torch.zeros(4, dtype=torch.int32)
     args = _attention_args(kv, monkeypatch, dev_err=word)
     assert (args["dev_err"], args["ws"], args["ws_bytes"]) == (word.data_ptr(), kv.ws.data_ptr(), 4096)
+
+
+@pytest.mark.parametrize("apart,fits", [(0, False), (16, False), (3 * 2 * 64 * 2 - 16, False), (3 * 2 * 64 * 2, True)])
+def test_read_outputs_that_overlap_are_refused(apart, fits):
+    """Keys and values written to the same memory would be a mixture of both (the call is turned away, or
+    goes on to the check of the device)."""
+    from bit_nf4_quantised_codebook_b200 import api, build
+    build.build()
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses: for machines without a GPU")
+    c = api._KVCache(4, 16, 2, 64, 0, 4096, 8192, 12288, 16384)
+    b = api._KVBatch(1, 2, 3, 32, 64, 128)
+    for k, v in ((1 << 20, (1 << 20) + apart), ((1 << 20) + apart, 1 << 20)):
+        status = api.lib().qlora_kv_read(c, b, k, v, None, None)
+        assert (status != 1) is fits
+    assert api.lib().qlora_kv_read(c, b, 1 << 20, None, None, None) != 1

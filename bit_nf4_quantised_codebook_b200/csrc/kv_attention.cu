@@ -21,13 +21,14 @@
 // the small integers they are multiples of), within 2^-11 for NF4, at a scale where their
 // errors cancel on average (see launch_kv_attention).  Each query row is
 // scaled by a power of two to a largest magnitude in [2^13, 2^14) and is then exact in
-// fp16 down to 2^-38 of it.  The softmax keeps a reference m per row (its running maximum
+// fp16 down to 2^-30 of it, and rounded to 2^-38 of it below.  The softmax keeps a reference m per row (its running maximum
 // when last renewed) and float32 weights P = 2^(s - m) and their sum.  Into the second
 // product go w = P * cV * F_b in fp16 (within 2^-12), F_b a scale per row and block that
 // gives the largest contribution so far a w of 2^6 when last renewed.  m and F_b are renewed
 // when some w passes 2^14 or the sum 2^100, which after the first tokens is rare: the usual
 // step needs no maximum and no rescaling.  What is below 2^-31 of the largest contribution to
-// a block is lost, whatever the constants' range.  All accumulators are float32.
+// a block is lost, whatever the constants' range, and so is a weight below 2^-126 of the
+// row's largest, which is 0 in float32.  All accumulators are float32.
 //
 // Work.  An item is one sequence x row tile (8 * NT rows: tokens x the query heads of one
 // key/value head) x key/value head, cut into steps of 128 tokens.  The steps of all items
@@ -37,12 +38,15 @@
 // memory at the end of its part of an item.  An item that several groups shared is joined
 // from their normalised parts, in order, by a second small kernel.
 //
-// Bound by the issue of the decoding: 2.9 instructions per element (one of them the lookup
-// and permute of a pair's half, a quarter the copies and the softmax), load/store pipe 68 %
-// and integer pipe 49 % busy.  64 sequences of 1 to 8192 tokens, 64 query and 8 key/value
-// heads of 128: 81 us, 3.73 TB/s of codes and constants (0.58 of the measured copy rate); one
-// sequence of 131071: 49 us.  Codes loaded straight into registers took 62 us for the latter
-// (one 32-byte sector per request), registers spilled beside a full shared memory 4 us.
+// Bound by the decoding's instructions and their latencies together, no unit being full: 2.9
+// instructions per element (one of them the lookup and permute of a pair's half, a quarter the
+// copies and the softmax), issue slots 64 %, load/store pipe 68 % and integer pipe 49 % busy with the
+// 16 warps that the registers allow, which wait for fixed latencies first of all.  64 sequences of 1
+// to 8192 tokens, 64 query and 8 key/value heads of 128: 81 us in a replayed graph (86 call by call),
+// 3.72 TB/s of codes and constants (0.58 of the measured copy rate); one sequence of 131071: 50 us.
+// Codes loaded straight into registers took 62 us for the latter (one 32-byte sector per request),
+// registers spilled beside a full shared memory 4 us.  The tiles of 16 rows and the heads of 256 spill
+// all the same (88 bytes a thread with heads of 128, 32 with 64 and 256); what that costs them is not measured.
 #include <atomic>
 #include <climits>
 #include <cstdint>
@@ -827,7 +831,9 @@ constexpr int kFewRows = 64;
 // more, none has more rows than its first token's and those above one token each.  Up to kSpreadRows
 // of those, the few-row kernel takes the whole call (right for any number of rows, each 16 of
 // them decoding the cache anew): the launches cost a call without use for them 11 us (16 sequences of
-// 4096 tokens, 40 rows each: 107 against 96 us).
+// 4096 tokens, 40 rows each: 107 against 96 us).  Sequences without rows are taken for ones with a
+// token here, since totals do not tell a prompt among empty slots from a batch of single tokens: 256
+// tokens over 8192 take 78 us alone or among 64 slots, 246 among 256 (the header says so).
 // Single tokens stay in the few-row kernel for any number of query heads: with 128 of them on one
 // key/value head, one sequence of 32768 tokens takes 32 us (many-row kernel: 71), 16 of 4096 48 us
 // (45); only 64 of 2048 would be better off there (81 against 59 us).

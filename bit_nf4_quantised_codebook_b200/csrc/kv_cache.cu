@@ -10,9 +10,9 @@
 // two units of both sides, all loads issued together.
 // Bound by HBM for prompts (2 + 17/32 bytes per element each way) and by the chain of
 // dependent loads token_start -> kv_len -> page_table -> data for single tokens.  Measured:
-// reading 60000 tokens of 8 heads of 128 takes 56 us (5.5 TB/s, 0.85 of the measured copy
-// rate); appending 8000 such tokens and reading them back 25 us (3.6 TB/s, the append bound by
-// 25 instructions per element); a step of 16 tokens of 32 heads 5 us for both.
+// in a replayed graph, reading 60000 tokens of 8 heads of 128 takes 57 us (5.4 TB/s, 0.84 of the
+// measured copy rate); appending 8000 such tokens 13 us (2.1 times its floor: 25 instructions per element)
+// and that and reading them back 25 us; a step of 16 tokens of 32 heads 5 us for both.
 //
 // Code of one element.  The code is #{i : float32(x / c) >= t_i}.  x and c are
 // bfloat16, so x / c is one of the ratios a / b * 2^-k of integers a < 256, b < 256,

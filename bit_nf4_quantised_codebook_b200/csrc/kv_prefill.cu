@@ -37,12 +37,15 @@
 // a key whose blocks lie more than 2^kNearBlocks apart: there, constants multiply float32 sums.  (Marked for
 // one block of 2^31, 4096 over 8192 takes 4.4 ms in place of 0.57.)
 //
-// Measured (4096 tokens x 4 query heads over 8192 cached, 8 key/value heads of 128): 0.56 ms,
-// 742 TFLOP/s of the visible pairs.  A step takes 5200 clocks, of which the tensor cores work
-// 2100: it is bound by the chain from one step of a row tile to the next (softmax, the two
-// products and their hand-overs) and by the decoding of the values between two products that use
-// them (2400).  An item starts and ends in 15000 clocks (queries, first keys, outputs), the kernel in
-// 10000.  Tried without gain: values in two stages (more decoding next to the softmax slows it as
+// Measured (4096 tokens x 4 query heads over 8192 cached, 8 key/value heads of 128): 0.58 ms,
+// 715 TFLOP/s of the visible pairs (0.55 without the guards of sums and references, which the
+// compiler schedules some 3 % worse; folding them into other steps changed nothing).  A step takes 5700
+// clocks, of which the tensor cores work 2100: no unit is near its limit (three chunks of 1400 tokens
+// together: issue slots 39 %, tensor pipe 28 %, ex2 unit 29 % busy), it is bound by the chain from one
+// step of a row tile to the next (softmax, the two products and their hand-overs) and by the decoding of
+// the values between two products that use them (2400).  An item starts and ends in 15000 clocks
+// (queries, first keys, outputs), the kernel in 10000.  With heads of 256 (68 bytes of registers
+// spilled a thread), 2048 tokens x 4 query heads over 4096, 4 key/value heads, take 0.26 ms.  Tried without gain: values in two stages (more decoding next to the softmax slows it as
 // much), scores in two halves (products of 64 columns), 20 warps, two passes of the softmax between
 // checks (spills, and with shared memory full a spilled register is a second-level cache access),
 // outputs turned through shared memory (the stores are faster, the steps slower).

@@ -409,6 +409,8 @@ typedef struct qlora_kv_cache {
  * and a page outside 0 .. num_pages - 1 set QLORA_DEVERR_KV_INDEX and are
  * clamped or skipped: no access leaves the buffers, and what belongs to that
  * sequence is unspecified.
+ * All three operators look at every sequence of a call with token rows, those
+ * without rows too; pages only where they are used.
  * batch <= QLORA_KV_MAX_BATCH; tokens <= 2^30, and so is kv_len.
  */
 #define QLORA_KV_MAX_BATCH 4096
@@ -464,8 +466,10 @@ qlora_status qlora_kv_attention_workspace_size(const qlora_kv_cache *cache, int 
  *   out[row][h] = sum_j softmax_j(scale * q . k_j) v_j,  k = v = level * absmax
  *                 (not rounded to bfloat16 in between)
  * over the positions j < kv_len[b] that the row at position p sees: j <= p when
- * causal != 0, and j > p - window when window > 0.  A row that sees nothing
- * (an empty sequence, a negative position) gives zeros.
+ * causal != 0, and j > p - window when window > 0.  A row that sees nothing (an
+ * empty sequence; with causal != 0, a negative position) gives zeros.  With
+ * causal == 0 a row at a negative position (kv_len < n_b) sees the whole
+ * sequence.  Negative positions are no error here, unlike in append and read.
  * Q: device bfloat16, strided like K above; q_heads is a multiple of `heads`
  * (q_heads / heads <= 128, tokens * q_heads / heads <= 2^30), and query head h
  * reads key/value head h / (q_heads / heads).  out: device bfloat16
@@ -475,6 +479,20 @@ qlora_status qlora_kv_attention_workspace_size(const qlora_kv_cache *cache, int 
  * the scores, and their rows become NaN); identical inputs give identical bits.
  * A non-finite stored constant or query makes the rows (and, for a value, the
  * 64 channels) that see it NaN and no others.
+ * The operands of the two products are fp16, chosen for the tensor cores:
+ *   queries     scaled by a power of two per row; exact down to 2^-30 of the
+ *               row's largest, rounded to 2^-38 of it below;
+ *   keys and    levels, exact for Int4, E2M1 and E3M0, within 2^-11 for NF4; in
+ *   values      sequences of many rows level * absmax, for NF4 2^-11 more;
+ *   weights     within 2^-11; a token that contributes less than 2^-23 of the
+ *               largest contribution to a block of 64 channels may be lost, and a
+ *               weight below 2^-126 of the row's largest counts as 0.
+ * For NF4 the outputs are off by 0.0018-0.0020 of their norm (0.0016 is the
+ * rounding to bfloat16; a float32 computation from the same codes has that).
+ * Which kernels run is decided from batch and tokens as if every sequence had a
+ * row: a call with a prompt should not carry slots without rows along (4096 rows
+ * over 8192 tokens, 32/8 heads of 128: 0.57 ms alone or among 256 slots, 3.8 ms
+ * among 4096).
  */
 qlora_status qlora_kv_attention(const qlora_kv_cache *cache, const qlora_kv_batch *batch, const uint16_t *Q,
                                 int q_heads, int64_t q_token_stride, int64_t q_head_stride, float scale, int causal,

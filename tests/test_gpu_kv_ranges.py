@@ -290,3 +290,37 @@ def test_key_blocks_of_very_different_sizes(dim, larger, n):
     assert (bound <= 0.02 * np.abs(want)).all()
     off = (np.abs(f64(out) - want) - bound).max()
     assert off <= 0, off
+
+
+def test_random_ranges_and_masks():
+    """Sizes, scores, zeros, masks and lengths drawn at random; every row against the oracle.  A weight
+    below 2^-126 of its row's largest is 0 in float32: what such tokens would add is allowed for."""
+    a = api()
+    for seed in range(200):
+        rng = np.random.default_rng(9000 + seed)
+        dim = int(rng.choice(DIMS))
+        step, blocks = _step(dim), dim // 64
+        group, heads = int(rng.choice([1, 4, 7])), int(rng.choice([1, 3, 160]))
+        length = int(rng.choice([1, 17, 90, step, 2 * step + 5, 3 * step + 70]))
+        n = int(min(rng.choice([1, 2, 5, 20, 60, 130]), length + 3))
+        causal, window = bool(rng.random() < 0.6), int(rng.choice([0, 0, 1, 40, 200]))
+        t = np.round(rng.uniform(-0.5, 0.5, length) * rng.choice([4, 20, 100, 250]))
+        span = int(rng.choice([0, 3, 8, 12, 30, 60, 100]))
+        shape = [(length, blocks), (length, 1), (1, blocks)][rng.integers(3)]
+        size = rng.choice([1.0, 1.25, 1.75], (length, blocks)) * 2.0 ** rng.integers(-span, span + 1, shape)
+        size[rng.random((length, blocks)) < rng.choice([0, 0.02, 0.3])] = 0.0
+        if rng.random() < 0.3:
+            size[:step] = 0.0
+        case = Case([n], [length], page_size=16, seed=seed)
+        signs = np.where(rng.random(dim) < 0.5, -1.0, 1.0)
+        c, K, V = _fill(a, t, size, heads, dim, signs, case)
+        Q = torch.ones(n, heads * group, dim, dtype=torch.bfloat16, device="cuda")
+        out = a.qlora_kv_attention(c, case.batch(a), Q, scale=_scale(dim), causal=causal, window=window)
+        want, bound = kv.attention(np.ones((n, 1, dim)), K, V, _scale(dim), causal, window, False)
+        pos, j = np.arange(length - n, length)[:, None], np.arange(length)
+        see = (j <= pos if causal else np.ones((n, length), bool)) & ((j > pos - window) if window else True)
+        below = np.where(see, t, -np.inf)
+        below = below - np.maximum(below.max(1, keepdims=True), -1e9)  # (-inf throughout where nothing is seen)
+        gone = np.where(see & (below < -124), 2.0 ** np.maximum(below, -1000.0), 0.0) @ np.abs(V[:, 0])
+        off = np.abs(f64(out) - want) - bound - 1.01 * gone[:, None]
+        assert np.all(off <= 0), (seed, off.max())
